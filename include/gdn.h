@@ -16,7 +16,7 @@
  *   - All tensors are dense, C-contiguous, row-major arrays in DEVICE memory
  *     of the current CUDA device (no host pointers): float32, except the
  *     projections' operands (hidden, x and the weight matrices), which are
- *     bf16 bit patterns where an entry point says so.
+ *     bf16 bit patterns or signed bytes where an entry point says so.
  *   - The caller allocates and frees every buffer. The library allocates no
  *     memory, never synchronises, and enqueues its kernels on `stream`
  *     (a cudaStream_t; NULL means the legacy default stream). Results are
@@ -33,7 +33,7 @@
  *     aligned, workspaces 256-byte aligned; the per-head scalars (beta,
  *     gate, a, b, A_log, dt_bias), norm_w and the optional status words need
  *     4-byte alignment.
- *   - Status words (gdn_prefill, gdn_linear_bf16*, gdn_forward_batch*,
+ *   - Status words (gdn_prefill, gdn_linear_*, gdn_forward_batch*,
  *     gdn_short_conv_*): an optional zero-initialised device uint32 into
  *     which a kernel ORs a bit if one of its bounded waits (2 s) ever gives
  *     up; the kernel then returns without hanging. NULL: not reported.
@@ -68,6 +68,12 @@ typedef enum gdn_status {
     GDN_ERR_CUDA = 6,        /* the CUDA runtime refused the launch            */
     GDN_ERR_ALIAS = 7        /* an output or in-place buffer overlaps another  */
 } gdn_status;
+
+/* Element types of the arguments that take more than one. */
+typedef enum gdn_dtype {
+    GDN_F32 = 0,
+    GDN_BF16 = 1
+} gdn_dtype;
 
 /* Static English text for a status code (never NULL). */
 const char *gdn_status_string(int status);
@@ -255,6 +261,76 @@ gdn_status gdn_linear_bf16(const void *x, const void *w, float *y, int64_t M, in
  */
 gdn_status gdn_linear_bf16_split_k(const void *x, const void *w, float *y, int64_t M, int64_t N,
                                    int64_t K, uint32_t *status, void *stream);
+
+/*
+ * The 8-bit projection path: rows of activations (or of weights) in signed
+ * 8-bit integers with one fp32 scale a row, and the projection of such rows.
+ * It has no counterpart on the source pages, whose projections use the
+ * model's own quantised weights; the layer's composition is that of
+ * gdn_linear_bf16 ("Red Lite dev15e -- complete recurrent DeltaNet layer
+ * composition", opening list).
+ *
+ * Rows are quantised symmetrically. With a the row, m = max |a_i|:
+ *   q_i = 127 a_i / m to the nearest integer, halves to even (the quotient is
+ *   decided exactly: a q never depends on rounding inside the kernel), so q
+ *   lies in [-127, 127] and q_i * scale stands for a_i.
+ *   m = 0:  q = 0, scale = 0.
+ *   a value of the row is infinite or NaN:  q = 0, scale = NaN, so that
+ *   every product of the row is NaN.
+ *
+ * gdn_quantize_i8 -- rows as they are: a = x, scale = m / 127. For the input
+ * of a projection by token, and for its weights [N][K] by output channel.
+ *   x      [M][D] fp32 or bf16 (x_type)
+ *   q      [M][D] int8;  scale [M]
+ *
+ * gdn_add_rms_norm_i8 -- the residual's addition and the RMS norm before it:
+ *   h = x + residual in fp32 (x alone where residual is NULL), rounded to
+ *       residual_type: the row that residual_out receives is the row that is
+ *       normalised
+ *   a = h * weight, rounded to fp32;  scale = m / (127 sqrt(mean(h^2) + eps))
+ * (q * scale then stands for h / rms * weight: the division by the row's rms
+ * is in the scale alone, so q does not depend on it.)
+ *   x            [M][D] fp32 or bf16 (x_type)
+ *   residual     [M][D] fp32 or bf16 (residual_type), or NULL
+ *   weight       [D] fp32, multiplies directly
+ *   residual_out [M][D] residual_type, or NULL: not written. It may be
+ *                `residual` itself (updated in place), and may overlap it in
+ *                no other way
+ *   q [M][D] int8;  scale [M]
+ * Both: D a multiple of 16, any size (rows of up to 32768 elements are read
+ * once, longer ones twice). Results do not depend on M or on the other rows.
+ * All pointers 16-byte aligned, except scale (4). q and scale may overlap
+ * nothing. M above 2^31 - 1 gives GDN_ERR_OVERFLOW; an unknown type
+ * GDN_ERR_UNSUPPORTED.
+ */
+gdn_status gdn_quantize_i8(const void *x, int x_type, int8_t *q, float *scale, int64_t M,
+                           int64_t D, void *stream);
+gdn_status gdn_add_rms_norm_i8(const void *x, int x_type, const void *residual,
+                               const float *weight, float eps, void *residual_out,
+                               int residual_type, int8_t *q, float *scale, int64_t M, int64_t D,
+                               void *stream);
+
+/*
+ * gdn_linear_i8 -- gdn_linear_bf16's projection with 8-bit integer operands:
+ *   y[m][n] = (sum_k x[m][k] w[n][k]) * x_scale[m] * w_scale[n]
+ * The sum is an exact 32-bit integer, converted to fp32 once and multiplied
+ * by x_scale and then by w_scale in fp32 (bf16 output: rounded once more). A
+ * result therefore never depends on M, on the other rows or on how the
+ * kernels tile and split the product.
+ *
+ *   x        [M][K] int8, any values;  x_scale [M]
+ *   w        [N][K] int8, any values;  w_scale [N]
+ *   y        [M][N] fp32 or bf16 (y_type)
+ *   K        a multiple of 16 (16-byte rows for the tensor-memory copies), at
+ *            most 131056 (the sum fits 32 bits), GDN_ERR_UNSUPPORTED
+ *            otherwise; K = 0 gives y = 0
+ *   status   as gdn_linear_bf16
+ * x, w and y 16-byte aligned, the scales 4-byte; y may overlap no argument.
+ * Limits: M <= 65535 * 128, and at most 2^28 tiles of 128 x 128.
+ */
+gdn_status gdn_linear_i8(const int8_t *x, const float *x_scale, const int8_t *w,
+                         const float *w_scale, void *y, int y_type, int64_t M, int64_t N,
+                         int64_t K, uint32_t *status, void *stream);
 
 /*
  * gdn_forward_batch -- the recurrent layer over T consecutive positions of

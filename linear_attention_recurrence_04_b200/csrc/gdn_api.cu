@@ -421,7 +421,100 @@ gdn_status linear_call(const char* fn, const void* x, const void* w, float* y, i
     return launched(split ? launch_linear_bf16_split(a, cs) : launch_linear_bf16(a, cs), fn);
 }
 
+bool known_type(int t) { return t == GDN_F32 || t == GDN_BF16; }
+
+// Checks shared by the two row entries; `norm` selects the one with the RMS
+// norm (and the residual).
+gdn_status rows_i8_call(const char* fn, bool norm, const void* x, int x_type,
+                        const void* residual, const float* weight, float eps,
+                        void* residual_out, int residual_type, int8_t* q, float* scale, int64_t M,
+                        int64_t D, void* stream) {
+    if (M < 0 || D < 0)
+        return fail(GDN_ERR_SHAPE, "%s: negative M=%lld D=%lld", fn, (long long)M, (long long)D);
+    if (D % 16 != 0)
+        return fail(GDN_ERR_UNSUPPORTED, "%s: D=%lld must be a multiple of 16", fn, (long long)D);
+    if (!known_type(x_type) || !known_type(residual_type))
+        return fail(GDN_ERR_UNSUPPORTED, "%s: unknown type %d or %d", fn, x_type, residual_type);
+    int64_t n = 0;
+    if (M > INT32_MAX || D > INT32_MAX || !mul_ok(M, D, &n) || n > INT64_MAX / 4)
+        return fail(GDN_ERR_OVERFLOW, "%s: M or D too large", fn);
+    if (n == 0) { g_last_error[0] = '\0'; return GDN_OK; }
+    if (!x || !q || !scale || (norm && !weight))
+        return fail(GDN_ERR_NULL, "%s: a tensor pointer is NULL", fn);
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4) || !aligned(residual, 16) ||
+        !aligned(residual_out, 16) || !aligned(weight, 16))
+        return fail(GDN_ERR_ALIGN, "%s: alignment rule violated", fn);
+    const int64_t rbytes = n * (residual_type == GDN_BF16 ? 2 : 4);
+    // residual_out may be the residual itself, which then counts once
+    const bool in_place = residual_out && residual_out == residual;
+    const Span ins[] = {{q, n, "q"}, {scale, M * 4, "scale"},
+                        {residual_out, rbytes, "residual_out"},
+                        {x, n * (x_type == GDN_BF16 ? 2 : 4), "x"},
+                        {in_place ? nullptr : residual, rbytes, "residual"},
+                        {weight, norm ? D * 4 : 0, "weight"}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < 6; ++j)
+            if (j != i && overlaps(ins[i], ins[j]))
+                return fail(GDN_ERR_ALIAS, "%s: %s overlaps %s", fn, ins[i].name, ins[j].name);
+    RowsI8Args a{x, x_type == GDN_BF16, residual, residual_out, residual_type == GDN_BF16, weight,
+                 eps, q, scale, M, D};
+    return launched(launch_rows_i8(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
 }  // namespace
+
+gdn_status gdn_quantize_i8(const void* x, int x_type, int8_t* q, float* scale, int64_t M,
+                           int64_t D, void* stream) {
+    NvtxRange nvtx_range("gdn_quantize_i8");
+    return rows_i8_call("gdn_quantize_i8", false, x, x_type, nullptr, nullptr, 0.0f, nullptr,
+                        GDN_F32, q, scale, M, D, stream);
+}
+
+gdn_status gdn_add_rms_norm_i8(const void* x, int x_type, const void* residual,
+                               const float* weight, float eps, void* residual_out,
+                               int residual_type, int8_t* q, float* scale, int64_t M, int64_t D,
+                               void* stream) {
+    NvtxRange nvtx_range("gdn_add_rms_norm_i8");
+    return rows_i8_call("gdn_add_rms_norm_i8", true, x, x_type, residual, weight, eps,
+                        residual_out, residual_type, q, scale, M, D, stream);
+}
+
+gdn_status gdn_linear_i8(const int8_t* x, const float* x_scale, const int8_t* w,
+                         const float* w_scale, void* y, int y_type, int64_t M, int64_t N,
+                         int64_t K, uint32_t* status, void* stream) {
+    NvtxRange nvtx_range("gdn_linear_i8");
+    const char* fn = "gdn_linear_i8";
+    if (M < 0 || N < 0 || K < 0)
+        return fail(GDN_ERR_SHAPE, "%s: negative M=%lld N=%lld K=%lld", fn, (long long)M,
+                    (long long)N, (long long)K);
+    if (K % 16 != 0 || K > kLinearI8MaxK)
+        return fail(GDN_ERR_UNSUPPORTED, "%s: K=%lld must be a multiple of 16 and at most %lld", fn,
+                    (long long)K, (long long)kLinearI8MaxK);
+    if (!known_type(y_type))
+        return fail(GDN_ERR_UNSUPPORTED, "%s: unknown type %d", fn, y_type);
+    int64_t mn = 0, mk = 0, nk = 0;
+    if (M > (int64_t)65535 * 128 || N > INT32_MAX / 2 ||
+        ((M + 127) / 128) * ((N + 127) / 128) > ((int64_t)1 << 28) || !mul_ok(M, N, &mn) ||
+        !mul_ok(M, K, &mk) || !mul_ok(N, K, &nk))
+        return fail(GDN_ERR_OVERFLOW, "%s: M or N too large", fn);
+    if (mn == 0) { g_last_error[0] = '\0'; return GDN_OK; }
+    if (!y || (K > 0 && (!x || !w || !x_scale || !w_scale)))
+        return fail(GDN_ERR_NULL, "%s: a tensor pointer is NULL", fn);
+    if (!aligned(y, 16) || !aligned(status, 4) ||
+        (K > 0 && (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scale, 4) ||
+                   !aligned(w_scale, 4))))
+        return fail(GDN_ERR_ALIGN, "%s: alignment rule violated", fn);
+    const int64_t y_bytes = mn * (y_type == GDN_BF16 ? 2 : 4);
+    const Span ins[] = {{x, mk, "x"}, {w, nk, "w"}, {x_scale, M * 4, "x_scale"},
+                        {w_scale, N * 4, "w_scale"}, {status, status ? 4 : 0, "status"}};
+    gdn_status st = check_spans(ins, 5, 0, Span{y, y_bytes, "y"});
+    if (st != GDN_OK) return st;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (K == 0)    // an empty sum: y = 0
+        return launched(cudaMemsetAsync(y, 0, static_cast<size_t>(y_bytes), cs), fn);
+    LinearI8Args a{x, x_scale, w, w_scale, y, y_type == GDN_BF16, M, N, K, status};
+    return launched(launch_linear_i8(a, cs), fn);
+}
 
 gdn_status gdn_layer_decode(const float* mixed_qkv, const float* z, const float* a,
                             const float* b, float* conv_ring, const float* conv_w,

@@ -71,6 +71,39 @@ struct LinearArgs {
     uint32_t* status;  // optional device word for timeout bits
 };
 
+// Rows to 8-bit integers with a scale a row (gdn_quantize_i8.cu); `weight`
+// null: no norm, and then no residual.
+struct RowsI8Args {
+    const void* x;          // [M][D] fp32 or bf16
+    bool x_bf16;
+    const void* residual;   // [M][D] or null
+    void* residual_out;     // [M][D] or null; may be `residual`
+    bool residual_bf16;
+    const float* weight;    // [D] or null
+    float eps;
+    int8_t* q;              // [M][D]
+    float* scale;           // [M]
+    int64_t M;
+    int64_t D;              // a multiple of 16
+};
+
+// y[M][N] = (x . w^T) * x_scale[m] * w_scale[n], 8-bit integers with exact
+// sums (gdn_linear_i8.cu).
+struct LinearI8Args {
+    const int8_t* x;        // [M][K]
+    const float* x_scale;   // [M]
+    const int8_t* w;        // [N][K]
+    const float* w_scale;   // [N]
+    void* y;                // [M][N] fp32 or bf16
+    bool y_bf16;
+    int64_t M;
+    int64_t N;
+    int64_t K;              // a multiple of 16, at most kLinearI8MaxK
+    uint32_t* status;
+};
+// The longest sum of products of two signed bytes that fits 32 bits.
+constexpr int64_t kLinearI8MaxK = (INT32_MAX / (128 * 128)) / 16 * 16;
+
 struct ForwardBatchArgs {
     const void* hidden;    // [B][T][D] bf16
     const void* w_qkv;     // [C][D] bf16
@@ -151,6 +184,8 @@ cudaError_t launch_linear_bf16(const LinearArgs& a, cudaStream_t stream);
 // differ from launch_linear_bf16's by accumulation order); M > 128, or a
 // product too small to split, goes to launch_linear_bf16.
 cudaError_t launch_linear_bf16_split(const LinearArgs& a, cudaStream_t stream);
+cudaError_t launch_rows_i8(const RowsI8Args& a, cudaStream_t stream);
+cudaError_t launch_linear_i8(const LinearI8Args& a, cudaStream_t stream);
 cudaError_t launch_forward_batch(const ForwardBatchArgs& a, cudaStream_t stream);
 cudaError_t launch_short_conv(const ShortConvArgs& a, cudaStream_t stream);
 

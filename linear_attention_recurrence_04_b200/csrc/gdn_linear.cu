@@ -54,6 +54,7 @@
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
 #include "gdn_tc.cuh"
+#include "gdn_tmap.h"
 
 // Tile shape: 0 chooses per launch; 64, 128 or 256 force 128 x that width;
 // 512 forces 256 x 256.
@@ -1198,26 +1199,6 @@ linear_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
     tc::cluster_sync();
     tc::tc_fence_after();
     if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
-}
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link
-// against libcuda).
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    return fn;
 }
 
 // Row-major bf16 matrix [rows][K] as a 2D tensor map with box [box_rows][64].

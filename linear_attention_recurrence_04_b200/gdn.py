@@ -34,7 +34,8 @@ EXPORTS = ("gdn_status_string", "gdn_last_error", "gdn_last_cuda_error", "gdn_st
            "gdn_forward_batch_workspace_size",
            "gdn_forward_batch", "gdn_forward_batch_noalloc", "gdn_short_conv_workspace_size",
            "gdn_short_conv_forward_batch", "gdn_short_conv_forward", "gdn_short_conv_pair",
-           "gdn_kda_step", "gdn_kda_prefill", "gdn_selftest_bounded_wait",
+           "gdn_kda_step", "gdn_kda_prefill", "gdn_quantize_i8", "gdn_add_rms_norm_i8",
+           "gdn_linear_i8", "gdn_selftest_bounded_wait",
            "gdn_selftest_grid_barrier")
 
 
@@ -96,6 +97,13 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     for name in ("gdn_kda_step", "gdn_kda_prefill"):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = [_VP] * 7 + [_I64] * 6 + [_VP]
+    lib.gdn_quantize_i8.restype = ctypes.c_int
+    lib.gdn_quantize_i8.argtypes = [_VP, ctypes.c_int, _VP, _VP, _I64, _I64, _VP]
+    lib.gdn_add_rms_norm_i8.restype = ctypes.c_int
+    lib.gdn_add_rms_norm_i8.argtypes = ([_VP, ctypes.c_int, _VP, _VP, _F32, _VP, ctypes.c_int]
+                                        + [_VP, _VP, _I64, _I64, _VP])
+    lib.gdn_linear_i8.restype = ctypes.c_int
+    lib.gdn_linear_i8.argtypes = [_VP] * 5 + [ctypes.c_int] + [_I64] * 3 + [_VP, _VP]
     lib.gdn_selftest_bounded_wait.restype = ctypes.c_int
     lib.gdn_selftest_bounded_wait.argtypes = [_VP, ctypes.c_uint64, ctypes.c_int, _VP]
     lib.gdn_selftest_grid_barrier.restype = ctypes.c_int
@@ -542,6 +550,117 @@ def short_conv_pair(hidden, w_in, w_out, conv_ring, scratch_ring, conv_w, out=No
                workspace.data_ptr(), workspace.numel(), B, D, K, sp, _stream(device, stream))
     _raise_on("gdn_short_conv_pair", st)
     return out
+
+
+# -- 8-bit projections ---------------------------------------------------------
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}    # gdn_dtype
+
+
+def _check(t, name, dtypes, shape, device):
+    """The device of `t` (checked against `device` where that is given)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.device
+
+
+_F32_ONLY, _I8_ONLY, _FLOATS = (torch.float32,), (torch.int8,), (torch.float32, torch.bfloat16)
+
+
+def _rows_args(x, q, scale):
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    device = _check(x, "x", _FLOATS, None, None)
+    lead = x.shape[:-1]
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.int8, device=device)
+    else:
+        _check(q, "q", _I8_ONLY, x.shape, device)
+    if scale is None:
+        scale = torch.empty(lead, dtype=torch.float32, device=device)
+    else:
+        _check(scale, "scale", _F32_ONLY, lead, device)
+    return device, lead.numel(), x.shape[-1], q, scale
+
+
+def quantize_i8(x, q=None, scale=None, *, stream=None):
+    """Rows of x [..., D] (fp32 or bf16, D a multiple of 16) in 8-bit integers
+    with one scale a row: activations by token, weights [N, K] by output
+    channel. Returns (q [..., D] int8, scale [...] fp32), q * scale ~ x."""
+    device, M, D, q, scale = _rows_args(x, q, scale)
+    st = _call(device, load_library().gdn_quantize_i8, x.data_ptr(), _DTYPES[x.dtype],
+               q.data_ptr(), scale.data_ptr(), M, D, _stream(device, stream))
+    _raise_on("gdn_quantize_i8", st)
+    return q, scale
+
+
+def add_rms_norm_i8(x, weight, residual=None, residual_out=None, q=None, scale=None, *,
+                    eps: float = 1e-6, stream=None):
+    """h = x + residual (x alone without one), rounded to the residual's type;
+    h / rms(h) * weight in 8-bit integers with one scale a row. x [..., D] fp32
+    or bf16, residual and residual_out [..., D] fp32 or bf16, weight [D] fp32.
+    residual_out receives h (it may be `residual`; a new tensor when only
+    `residual` is given). Returns (q, scale, residual_out or None)."""
+    device, M, D, q, scale = _rows_args(x, q, scale)
+    _check(weight, "weight", _F32_ONLY, x.shape[-1:], device)
+    rtype = 0
+    if residual is not None:
+        _check(residual, "residual", _FLOATS, x.shape, device)
+        rtype = _DTYPES[residual.dtype]
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+    if residual_out is not None:
+        _check(residual_out, "residual_out",
+               _FLOATS if residual is None else (residual.dtype,), x.shape, device)
+        rtype = _DTYPES[residual_out.dtype]
+    st = _call(device, load_library().gdn_add_rms_norm_i8, x.data_ptr(), _DTYPES[x.dtype],
+               None if residual is None else residual.data_ptr(), weight.data_ptr(), eps,
+               None if residual_out is None else residual_out.data_ptr(), rtype, q.data_ptr(),
+               scale.data_ptr(), M, D, _stream(device, stream))
+    _raise_on("gdn_add_rms_norm_i8", st)
+    return q, scale, residual_out
+
+
+def linear_i8(x, x_scale, w, w_scale, y=None, *, out_dtype=torch.float32, status=None,
+              stream=None):
+    """y = (x @ w.T) * x_scale[..., None] * w_scale: x [..., K] int8 with x_scale
+    [...], w [N, K] int8 with w_scale [N], exact integer sums (K a multiple of
+    16, at most 131056). y [..., N] has `out_dtype` (fp32 or bf16), or its own
+    type when given. `status` as for linear_bf16."""
+    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
+        raise ValueError("x must be [..., K] and w [N, K]")
+    N, K = w.shape
+    device = _check(x, "x", _I8_ONLY, None, None)
+    lead = x.shape[:-1]
+    _check(x_scale, "x_scale", _F32_ONLY, lead, device)
+    _check(w, "w", _I8_ONLY, None, device)
+    _check(w_scale, "w_scale", _F32_ONLY, w.shape[:1], device)
+    if y is None:
+        if out_dtype not in _DTYPES:
+            raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+        y = torch.empty(lead + (N,), dtype=out_dtype, device=device)
+    else:
+        _check(y, "y", _FLOATS, lead + (N,), device)
+    sp = None
+    if status is not None:
+        if status.dtype is not torch.int32 or status.device != device or status.numel() != 1:
+            raise TypeError("status must be a one-element int32 tensor on the same device")
+        sp = status.data_ptr()
+    st = _call(device, load_library().gdn_linear_i8, x.data_ptr(), x_scale.data_ptr(),
+               w.data_ptr(), w_scale.data_ptr(), y.data_ptr(), _DTYPES[y.dtype], lead.numel(), N,
+               K, sp, _stream(device, stream))
+    _raise_on("gdn_linear_i8", st)
+    return y
 
 
 # -- failure detection -------------------------------------------------------

@@ -1,0 +1,350 @@
+"""The 8-bit projection path (gdn_quantize_i8, gdn_add_rms_norm_i8,
+gdn_linear_i8) on the GPU against its definition in numpy.
+
+The integers are decided exactly by the definition, and the product's sums are
+exact, so integers, residuals and products are compared bit for bit. Scales are
+formed in double and rounded to fp32 once: half a step, 2^-24 relative, plus
+the double sum's own error (D 2^-53 for D up to 131056: below 2^-35)."""
+import numpy as np
+import pytest
+import torch
+
+import i8_reference as ref
+import oracle
+from linear_attention_recurrence_04_b200 import gdn, inputs
+from parity import assert_parity
+
+pytestmark = pytest.mark.gpu
+
+SCALE_RTOL = 2.0 ** -24 * (1 + 2.0 ** -10)
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def draw_rows(M, D, seed, dtype=F32):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, D, generator=g) * torch.exp(torch.randn(M, 1, generator=g))
+    x = torch.where(torch.rand(1, D, generator=g) < 0.02, 10 * x, x)
+    return x.to(dtype)
+
+
+def check_rows(q, scale, want_q, want_scale):
+    torch.cuda.synchronize()
+    assert np.array_equal(q.cpu().numpy(), want_q)
+    s = scale.cpu().numpy().astype(np.float64)
+    assert np.array_equal(np.isnan(s), np.isnan(want_scale))
+    ok = ~np.isnan(s)
+    # a scale below the least normal fp32 is off by half a step of 2^-149
+    assert np.all(np.abs(s[ok] - want_scale[ok]) <= np.maximum(want_scale[ok] * SCALE_RTOL, 2.0 ** -150))
+
+
+SHAPES = [(1, 16), (3, 16), (300, 48), (1, 2048), (5, 4112), (130, 2048), (33, 8192), (2, 16384),
+          (2, 32768), (3, 32784), (1, 131056), (0, 64), (4, 0)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,D", SHAPES)
+def test_quantize(M, D, dtype):
+    x = draw_rows(M, D, seed=M + D, dtype=dtype)
+    q, s = gdn.quantize_i8(x.cuda())
+    if M * D:
+        check_rows(q, s, *ref.rows(x.float().numpy())[:2])
+    assert q.shape == (M, D) and s.shape == (M,)
+
+
+@pytest.mark.parametrize("res", [None, F32, BF16])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,D", SHAPES)
+def test_add_rms_norm(M, D, dtype, res):
+    x = draw_rows(M, D, seed=M + D, dtype=dtype)
+    r = None if res is None else 3 * draw_rows(M, D, seed=M + D + 1, dtype=res)
+    w = 1 + 0.2 * draw_rows(1, max(D, 1), seed=5)[0, :D]
+    q, s, h = gdn.add_rms_norm_i8(x.cuda(), w.cuda(), None if r is None else r.cuda(), eps=1e-5)
+    if M * D:
+        wq, ws, wh = ref.rows(x.float().numpy(), None if r is None else r.float().numpy(), w.numpy(),
+                              1e-5, res is BF16)
+        check_rows(q, s, wq, ws)
+        if r is not None:
+            assert h.dtype == res and np.array_equal(h.float().cpu().numpy(), wh)
+    assert (h is None) == (r is None)
+
+
+@pytest.mark.parametrize("M,D", [(7, 2048), (2, 32784)])
+def test_add_rms_norm_in_place_and_first_layer(M, D):
+    """residual_out may be the residual; without a residual it receives the
+    row in its own type, and the norm reads that rounded row."""
+    x, r = draw_rows(M, D, 1), draw_rows(M, D, 2, BF16)
+    w = torch.ones(D)
+    wq, ws, wh = ref.rows(x.numpy(), r.float().numpy(), w.numpy(), residual_bf16=True)
+    rc = r.cuda()
+    q, s, h = gdn.add_rms_norm_i8(x.cuda(), w.cuda(), rc, rc)
+    check_rows(q, s, wq, ws)
+    assert h is rc and np.array_equal(rc.float().cpu().numpy(), wh)
+    out = torch.empty(M, D, dtype=BF16, device="cuda")
+    q, s, h = gdn.add_rms_norm_i8(x.cuda(), w.cuda(), residual_out=out)
+    wq, ws, wh = ref.rows(x.numpy(), None, w.numpy(), residual_bf16=True)
+    check_rows(q, s, wq, ws)
+    assert np.array_equal(out.float().cpu().numpy(), wh)
+
+
+def special_rows(D=64):
+    x = np.zeros((14, D), np.float32)
+    g = np.random.default_rng(3)
+    x[1:] = g.standard_normal((13, D))
+    x[2, 5] = np.nan
+    x[3, 7] = np.inf
+    x[4, 9] = -np.inf
+    x[5] *= 1e-42                                  # subnormal
+    x[6] *= 1e-31
+    x[7] *= np.float32(1e38)
+    x[8] = 0
+    x[8, 3] = 1e-45                                # the least positive number alone
+    x[9] = -x[9, 0]                                # every value the largest
+    x[10, 1:] = 0
+    x[11, :] = -0.0
+    x[12, 0] = np.finfo(np.float32).max            # the largest number
+    x[13, 2], x[13, 3] = np.nan, np.inf
+    return x
+
+
+def test_special_values():
+    """Zero rows, infinities and NaN, subnormal and huge rows."""
+    x = special_rows()
+    q, s = gdn.quantize_i8(torch.from_numpy(x).cuda())
+    check_rows(q, s, *ref.rows(x)[:2])
+    s = s.cpu().numpy()
+    assert s[0] == 0 and s[11] == 0 and np.isnan(s[[2, 3, 4, 13]]).all()
+    w = np.ones(x.shape[1], np.float32)
+    q, s, h = gdn.add_rms_norm_i8(torch.from_numpy(x).cuda(), torch.from_numpy(w).cuda(),
+                                  residual_out=torch.empty(x.shape, device="cuda"))
+    check_rows(q, s, *ref.rows(x, None, w)[:2])
+    assert np.array_equal(h.cpu().numpy(), x, equal_nan=True)
+    # a residual that brings the NaN; a weight of zero leaves an empty row
+    r = np.zeros_like(x)
+    r[1, 1] = np.nan
+    q, s, _ = gdn.add_rms_norm_i8(torch.from_numpy(x).cuda(), torch.from_numpy(0 * w).cuda(),
+                                  torch.from_numpy(r).cuda())
+    check_rows(q, s, *ref.rows(x, r, 0 * w)[:2])
+    # the products of a row that is not finite are NaN, of an empty row zero
+    qx, sx = gdn.quantize_i8(torch.from_numpy(x).cuda())
+    y = gdn.linear_i8(qx, sx, torch.ones(3, 64, dtype=torch.int8, device="cuda"),
+                      torch.ones(3, device="cuda")).cpu().numpy()
+    assert np.isnan(y[[2, 3, 4, 13]]).all() and (y[[0, 11]] == 0).all()
+
+
+def test_borders():
+    """Values on a half and one step to either side of it: with m = 254 s and
+    a = (2 k + 1) s, 127 a / m is exactly k + 1/2."""
+    rows = []
+    for s in (1.0, 3.0, 0.1, 8388607.0, 1e-20, 1.7e-36, 1e30):
+        s = np.float32(s)
+        s = np.float32(s - np.fmod(s, np.spacing(s) * 256))   # (2 k + 1) s and 254 s exact
+        k = np.arange(127, dtype=np.float32)
+        a = (2 * k + 1) * s
+        row = np.concatenate([[254 * s], a, np.nextafter(a, np.float32(0)),
+                              np.nextafter(a, np.float32(np.inf)), -a]).astype(np.float32)
+        rows.append(np.pad(row, (0, 512 - row.size)))
+    x = np.stack(rows)
+    q, s = gdn.quantize_i8(torch.from_numpy(x).cuda())
+    check_rows(q, s, *ref.rows(x)[:2])
+    assert (ref.rows(x)[0][0, 1:128] == np.rint(np.arange(127) + 0.5)).all()
+
+
+def test_rows_independent_of_batch():
+    x = draw_rows(1000, 2048, 9).cuda()
+    q, s = gdn.quantize_i8(x)
+    w = torch.ones(2048, device="cuda")
+    qn, sn, _ = gdn.add_rms_norm_i8(x, w)
+    for r in (0, 499, 999):
+        q1, s1 = gdn.quantize_i8(x[r:r + 1].contiguous())
+        assert torch.equal(q1[0], q[r]) and torch.equal(s1[0], s[r])
+        q1, s1, _ = gdn.add_rms_norm_i8(x[r:r + 1].contiguous(), w)
+        assert torch.equal(q1[0], qn[r]) and torch.equal(s1[0], sn[r])
+
+
+# -- the product ------------------------------------------------------------------
+
+def draw_product(M, N, K, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randint(-128, 128, (M, K), generator=g, dtype=torch.int8)
+    w = torch.randint(-128, 128, (N, K), generator=g, dtype=torch.int8)
+    sx = torch.exp(torch.randn(M, generator=g)) / 127
+    sw = torch.exp(torch.randn(N, generator=g)) / 127 / max(K, 1) ** 0.5
+    return x, sx, w, sw
+
+
+def check_product(M, N, K, dtype, seed=0, rows=None):
+    x, sx, w, sw = draw_product(M, N, K, seed + M + 3 * N + 7 * K)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pad = torch.full(((M + 2) * N + 8,), 7.0, dtype=dtype, device="cuda")
+    y = gdn.linear_i8(x.cuda(), sx.cuda(), w.cuda(), sw.cuda(), pad[:M * N].view(M, N),
+                      status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert (pad[M * N:] == 7.0).all(), "written behind the last row"
+    rows = slice(None) if rows is None else rows
+    want = ref.linear(x.numpy()[rows], sx.numpy()[rows], w.numpy(), sw.numpy(), dtype is BF16)
+    got = y.float().cpu().numpy()[rows]
+    assert np.array_equal(got, want), np.argwhere(got != want)[:4].tolist()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 16), (1, 8, 16), (2, 1, 2048), (3, 5, 144), (1, 8192, 2048), (15, 130, 1040),
+    (16, 128, 128), (17, 127, 256), (33, 64, 2048), (64, 4096, 2048), (65, 2050, 512),
+    (100, 300, 4096), (128, 257, 1008), (129, 64, 2048), (200, 1000, 272), (255, 255, 400),
+    (256, 64, 2048), (300, 4100, 1040), (513, 2048, 4096), (777, 2050, 1040), (2049, 33, 160),
+])
+def test_linear(M, N, K, dtype):
+    check_product(M, N, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_linear_pair_tiles_ragged(dtype):
+    """Enough tiles for every pair of SMs, no size on the tile grid."""
+    check_product(2500, 2602, 400, dtype)
+    check_product(2501, 2603, 16, dtype)
+
+
+def test_linear_large_sampled():
+    check_product(4096, 8192, 2048, F32, rows=[0, 1, 127, 128, 2049, 4095])
+
+
+def test_linear_many_tiles_a_pair():
+    """Several tiles for each pair of SMs: both accumulator sets in turn."""
+    check_product(9000, 4100, 48, BF16, rows=list(range(0, 9000, 37)) + [8999])
+
+
+def test_linear_longest_sums():
+    """K at its limit, every product 128 * 128: the largest 32-bit sum."""
+    K = 131056
+    x = torch.full((3, K), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((5, K), -128, dtype=torch.int8, device="cuda")
+    one = torch.ones(5, device="cuda")
+    y = gdn.linear_i8(x, one[:3], w, one)
+    assert (y.cpu().numpy() == np.float32(K * 16384)).all()
+
+
+def test_linear_empty():
+    x = torch.zeros(3, 0, dtype=torch.int8, device="cuda")
+    w = torch.zeros(5, 0, dtype=torch.int8, device="cuda")
+    y = torch.full((3, 5), 7.0, device="cuda")
+    gdn.linear_i8(x, torch.ones(3, device="cuda"), w, torch.ones(5, device="cuda"), y)
+    assert torch.count_nonzero(y) == 0
+    e = gdn.linear_i8(torch.zeros(0, 16, dtype=torch.int8, device="cuda"), torch.ones(0, device="cuda"),
+                      torch.zeros(5, 16, dtype=torch.int8, device="cuda"), torch.ones(5, device="cuda"))
+    assert e.shape == (0, 5)
+
+
+def test_linear_rows_independent_of_batch():
+    """A row is the same in every call, whatever form computes it."""
+    x, sx, w, sw = (t.cuda() for t in draw_product(4096, 4096, 1024, 13))
+    y = gdn.linear_i8(x, sx, w, sw)
+    for M in (1, 20, 64, 128, 200, 700):
+        assert torch.equal(gdn.linear_i8(x[-M:], sx[-M:], w, sw), y[-M:]), M
+
+
+# -- as they are used ---------------------------------------------------------------
+
+def test_chain_on_a_stream_captured_and_replayed():
+    """norm -> product -> quantise -> product on a side stream, captured once
+    and replayed on new inputs, two graphs of other buffers interleaved."""
+    M, D, N = 5, 2048, 4096
+    g = torch.Generator().manual_seed(4)
+    w1, w2 = torch.randn(N, D, generator=g).cuda(), torch.randn(D, N, generator=g).cuda()
+    q1, s1 = gdn.quantize_i8(w1)
+    q2, s2 = gdn.quantize_i8(w2)
+    norm_w = torch.ones(D, device="cuda")
+    torch.cuda.synchronize()
+
+    def chain(x, r, out, stream=None):
+        q, s, _ = gdn.add_rms_norm_i8(x, norm_w, r, r, stream=stream)
+        y = gdn.linear_i8(q, s, q1, s1, stream=stream)
+        q, s = gdn.quantize_i8(y, stream=stream)
+        gdn.linear_i8(q, s, q2, s2, out, stream=stream)
+
+    bufs, graphs = [], []
+    for i in range(2):
+        x, r = torch.randn(M, D, device="cuda"), torch.zeros(M, D, device="cuda")
+        out = torch.empty(M, D, device="cuda")
+        chain(x, r, out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chain(x, r, out)
+        bufs.append((x, r, out))
+        graphs.append(graph)
+    side = torch.cuda.Stream()
+    for it in range(4):
+        new = [torch.randn(M, D, generator=torch.Generator().manual_seed(it * 2 + i)) for i in range(2)]
+        old = []
+        for (x, r, out), n in zip(bufs, new):
+            x.copy_(n)
+            old.append(r.clone())
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for (x, r, out), o in zip(bufs, old):
+            want_r, want = o.clone(), torch.empty(M, D, device="cuda")
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                chain(x, want_r, want)
+            side.synchronize()
+            assert torch.equal(want, out) and torch.equal(want_r, r)
+    graphs.clear()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams share nothing."""
+    a = [t.cuda() for t in draw_product(64, 4096, 2048, 1)]
+    b = [t.cuda() for t in draw_product(700, 2050, 1040, 2)]
+    want = [gdn.linear_i8(*a), gdn.linear_i8(*b)]
+    outs = [[torch.empty_like(w) for _ in range(8)] for w in want]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(8):
+        for args, o, st in zip((a, b), outs, streams):
+            gdn.linear_i8(*args, o[i], stream=st)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(t, w) for t in o)
+
+
+def test_layer_decode_with_8_bit_projections():
+    """One token through a whole recurrent layer: norm with the residual, the
+    qkv, z and b | a projections, the fused layer, the output projection. The
+    integer stages are compared bit for bit with the definition, the fused
+    layer with the oracle, each from the stage before it."""
+    B, D, Hk, Hv = 6, 512, 16, 32
+    C, HD = 2 * Hk * 128 + Hv * 128, Hv * 128
+    d = inputs.forward_inputs(B, 1, D=D, seed=77, state_std=0.05)
+    t = {k: torch.from_numpy(np.ascontiguousarray(v)).cuda() for k, v in d.items()}
+    x, r = draw_rows(B, D, 31), draw_rows(B, D, 32, BF16)
+    norm_w = 1 + 0.1 * draw_rows(1, D, 33)[0]
+    wq = {k: gdn.quantize_i8(t[k].float()) for k in ("w_qkv", "w_z", "w_ba", "w_out")}
+    q, s, h = gdn.add_rms_norm_i8(x.cuda(), norm_w.cuda(), r.cuda())
+    p = {k: gdn.linear_i8(q, s, *wq[k]) for k in ("w_qkv", "w_z", "w_ba")}
+    b, a = p["w_ba"][:, :Hv].contiguous(), p["w_ba"][:, Hv:].contiguous()
+    ring0, state0 = d["conv_ring"].copy(), d["state"].copy()
+    y = gdn.layer_decode(p["w_qkv"], p["w_z"], a, b, t["conv_ring"], t["conv_w"], t["A_log"],
+                         t["dt_bias"], t["norm_w"], t["state"], Hk=Hk)
+    qy, sy = gdn.quantize_i8(y)
+    out = gdn.linear_i8(qy, sy, *wq["w_out"], out_dtype=BF16)
+    torch.cuda.synchronize()
+
+    n = lambda v: v.float().cpu().numpy()  # noqa: E731
+    for k in wq:
+        check_rows(*wq[k], *ref.rows(n(t[k]))[:2])
+    rq, rs, rh = ref.rows(x.numpy(), r.float().numpy(), norm_w.numpy(), residual_bf16=True)
+    check_rows(q, s, rq, rs)
+    assert np.array_equal(n(h), rh)
+    for k in p:
+        assert np.array_equal(n(p[k]), ref.linear(q.cpu().numpy(), n(s), wq[k][0].cpu().numpy(), n(wq[k][1])))
+    o = oracle.load()
+    oy, oring, ostate = o.layer_decode(n(p["w_qkv"]), n(p["w_z"]), n(a), n(b), ring0, d["conv_w"],
+                                       d["A_log"], d["dt_bias"], d["norm_w"], state0, Hk=Hk)
+    assert_parity(n(y), oy, "layer output")
+    assert_parity(n(t["state"]), ostate, "state")
+    check_rows(qy, sy, *ref.rows(n(y))[:2])
+    assert np.array_equal(n(out), ref.linear(qy.cpu().numpy(), n(sy), wq["w_out"][0].cpu().numpy(),
+                                             n(wq["w_out"][1]), True))
