@@ -25,6 +25,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
@@ -35,7 +36,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kBK = 128;                     // bytes of K a stage: one swizzle row
+constexpr int kAtom = 128;                   // bytes of K in a swizzled row
 constexpr int kRows = 128;                   // output channels of a split tile
 constexpr int kThreads = 192;                // producer, MMA and four epilogue warps
 constexpr int kMaxSplits = 8;                // CTAs of a cluster
@@ -56,12 +57,71 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
     *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(b);
 }
 
+// 32 bytes (a whole sector) at once, past L1: nothing here reads it again.
+__device__ __forceinline__ void store32b(void* p, const uint32_t (&u)[8]) {
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]),
+                   "r"(u[6]), "r"(u[7]) : "memory");
+}
+__device__ __forceinline__ uint32_t bits2(float a, float b) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+// The first `n` (a whole number of 32-byte pieces) of a token's 32 channels.
+__device__ __forceinline__ void store32(float* p, const float (&v)[32], int n) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+        const uint32_t u[8] = {__float_as_uint(v[j]),     __float_as_uint(v[j + 1]),
+                               __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3]),
+                               __float_as_uint(v[j + 4]), __float_as_uint(v[j + 5]),
+                               __float_as_uint(v[j + 6]), __float_as_uint(v[j + 7])};
+        if (j < n) store32b(p + j, u);
+    }
+}
+__device__ __forceinline__ void store32(__nv_bfloat16* p, const float (&v)[32], int n) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 16) {
+        const uint32_t u[8] = {bits2(v[j], v[j + 1]),       bits2(v[j + 2], v[j + 3]),
+                               bits2(v[j + 4], v[j + 5]),   bits2(v[j + 6], v[j + 7]),
+                               bits2(v[j + 8], v[j + 9]),   bits2(v[j + 10], v[j + 11]),
+                               bits2(v[j + 12], v[j + 13]), bits2(v[j + 14], v[j + 15])};
+        if (j < n) store32b(p + j, u);
+    }
+}
+// v[j] of lane i becomes v[i] of lane j: at each step the lanes that differ in
+// one bit swap the halves of their values that differ in it.
+__device__ __forceinline__ void transpose32(float (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if ((j & o) == 0) {
+                const float got = __shfl_xor_sync(kFull, up ? v[j] : v[j | o], o);
+                if (up) v[j] = got; else v[j | o] = got;
+            }
+        }
+    }
+}
+
+// A wait that ran out: reported, and seen by the CTA's other warps.
+__device__ __forceinline__ void give_up(uint32_t* status, uint32_t bit, int* failed) {
+    if ((threadIdx.x & 31) == 0) {
+        if (status) atomicOr(status, bit);
+        atomicExch(failed, 1);
+    }
+    __syncwarp();
+}
+
 // ---- split form --------------------------------------------------------------
 template <int MC>
 struct SplitSmem {
-    static constexpr uint32_t kW = kRows * kBK;
-    static constexpr uint32_t kStage = kW + MC * kBK;
-    static constexpr int kStages = (196608 / kStage) < 10 ? static_cast<int>(196608 / kStage) : 10;
+    static constexpr int kAtoms = 2;                          // of K a stage
+    static constexpr uint32_t kW = kRows * kAtom;             // one atom of each operand
+    static constexpr uint32_t kX = MC * kAtom;
+    static constexpr uint32_t kStage = kAtoms * (kW + kX);
+    static constexpr int kStages = 196608 / kStage;
     static constexpr uint32_t kRing = kStage * kStages;
     static constexpr uint32_t kPart = MC * kRows * 4;         // the parked partial tile
     static constexpr size_t kDynamic = (kRing > kPart ? kRing : kPart) + 1024;
@@ -81,6 +141,7 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
     __shared__ __align__(8) uint64_t full[kStages];
     __shared__ __align__(8) uint64_t empty[kStages];
     __shared__ __align__(8) uint64_t acc_full;
+    __shared__ __align__(16) float sx_s[4][MC];        // the tokens' scales, for each epilogue warp
     __shared__ uint32_t tmem_slot;
     __shared__ int issued, consumed;
     __shared__ int failed;
@@ -89,18 +150,21 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
     const uint32_t base = (raw + 1023u) & ~1023u;
     int* part = reinterpret_cast<int*>(smem_raw + (base - raw));   // [MC][128], after the MMAs
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = tc::warp_index();
     const int lane = threadIdx.x & 31;
     const int rank = static_cast<int>(blockIdx.x) % splits;
     const int n_tiles = (N + kRows - 1) / kRows;
     const int tile = static_cast<int>(blockIdx.x) / splits;
     const int n0 = (tile % n_tiles) * kRows;
     const int m0 = (tile / n_tiles) * MC;
+    constexpr int kBK = L::kAtoms * kAtom;
     const int n_kt = (K + kBK - 1) / kBK;
     const int kb = static_cast<int>(static_cast<int64_t>(rank) * n_kt / splits);
     const int ke = static_cast<int>(static_cast<int64_t>(rank + 1) * n_kt / splits);
 
     if (threadIdx.x == 0) {
+        tc::prefetch_tmap(&tmap_x);
+        tc::prefetch_tmap(&tmap_w);
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(tc::smem_u32(&full[s]), 1);
             tc::mbar_init(tc::smem_u32(&empty[s]), 1);
@@ -120,67 +184,88 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot;
     tc::grid_dep_launch();
+    int done = 0;                                      // k-steps issued, or consumed
 
-    if (warp == 0 && lane == 0) {
-        tc::prefetch_tmap(&tmap_x);
-        tc::prefetch_tmap(&tmap_w);
-        // the first weight boxes head for L2 while the previous kernel ends
-        for (int kt = kb; kt < ke && kt < kb + 2; ++kt) tc::tma_prefetch_l2_2d(&tmap_w, kt * kBK, n0);
+    if (warp == 0) {
+        if (tc::elect_one()) {
+            // the first weight boxes head for L2 while the previous kernel ends
+            tc::tma_prefetch_l2_2d(&tmap_w, kb * kBK, n0);
+            tc::tma_prefetch_l2_2d(&tmap_w, kb * kBK + kAtom, n0);
+        }
         tc::grid_dep_wait();
         int s = 0;
         uint32_t ph = 1;                               // the ring starts empty
+        bool ready = true;
         for (int kt = kb; kt < ke; ++kt) {
-            const uint32_t fb = tc::smem_u32(&full[s]);
-            if (!tc::mbar_wait(tc::smem_u32(&empty[s]), ph)) {
-                if (status) atomicOr(status, tc::kTimeoutProducer);
-                atomicExch(&failed, 1);
+            if (!__all_sync(kFull, ready) && !tc::mbar_wait_warp(tc::smem_u32(&empty[s]), ph)) {
+                give_up(status, tc::kTimeoutProducer, &failed);
                 break;
             }
+            const uint32_t fb = tc::smem_u32(&full[s]);
             const uint32_t a = base + s * L::kStage;
-            tc::mbar_arrive_expect_tx(fb, L::kStage);
-            tc::tma_load_2d(a, &tmap_w, fb, kt * kBK, n0);
-            tc::tma_load_2d(a + L::kW, &tmap_x, fb, kt * kBK, m0);
-            issued = kt - kb + 1;
             if (++s == kStages) { s = 0; ph ^= 1; }
+            ready = tc::mbar_test_wait(tc::smem_u32(&empty[s]), ph);   // answered by the next pass
+            if (tc::elect_one()) {
+                tc::mbar_arrive_expect_tx(fb, L::kStage);
+#pragma unroll
+                for (int i = 0; i < L::kAtoms; ++i) {
+                    tc::tma_load_2d(a + i * L::kW, &tmap_w, fb, kt * kBK + i * kAtom, n0);
+                    tc::tma_load_2d(a + L::kAtoms * L::kW + i * L::kX, &tmap_x, fb,
+                                    kt * kBK + i * kAtom, m0);
+                }
+            }
+            ++done;
         }
-    } else if (warp == 1 && lane == 0) {
+        if (lane == 0) issued = done;
+    } else if (warp == 1) {
         tc::grid_dep_wait();
         const uint32_t idesc = tc::idesc_s8_s32(kRows, MC);
         int s = 0;
         uint32_t ph = 0;
-        bool ok = true;
+        bool ready = false;
         for (int kt = kb; kt < ke; ++kt) {
-            if (!tc::mbar_wait(tc::smem_u32(&full[s]), ph)) {
-                if (status) atomicOr(status, tc::kTimeoutMma);
-                atomicExch(&failed, 1);
-                ok = false;
+            if (!__all_sync(kFull, ready) && !tc::mbar_wait_warp(tc::smem_u32(&full[s]), ph)) {
+                give_up(status, tc::kTimeoutMma, &failed);
                 break;
             }
-            consumed = kt - kb + 1;
             tc::tc_fence_after();
             const uint64_t a = tc::desc_k_sw128(base + s * L::kStage);
-            const uint64_t b = tc::desc_k_sw128(base + s * L::kStage + L::kW);
-#pragma unroll
-            for (int kk = 0; kk < kBK / 32; ++kk)      // 32 bytes on: the address field counts 16s
-                tc::mma_i8(tmem, a + 2 * kk, b + 2 * kk, idesc, (kt > kb || kk > 0) ? 1u : 0u);
-            tc::mma_commit(tc::smem_u32(&empty[s]));
+            const uint64_t b = tc::desc_k_sw128(base + s * L::kStage + L::kAtoms * L::kW);
+            const uint32_t eb = tc::smem_u32(&empty[s]);
             if (++s == kStages) { s = 0; ph ^= 1; }
+            ready = tc::mbar_test_wait(tc::smem_u32(&full[s]), ph);
+            if (tc::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < kBK / 32; ++kk) {    // 32 bytes on: addresses count 16s
+                    const int i = kk / 4, o = 2 * (kk % 4);
+                    tc::mma_i8(tmem, a + (i * L::kW >> 4) + o, b + (i * L::kX >> 4) + o, idesc,
+                               (kt > kb || kk > 0) ? 1u : 0u);
+                }
+                tc::mma_commit(eb);
+                if (kt == ke - 1) tc::mma_commit(tc::smem_u32(&acc_full));
+            }
+            ++done;
         }
-        if (ok) tc::mma_commit(tc::smem_u32(&acc_full));
+        if (lane == 0) consumed = done;
     } else if (warp >= 2) {
         tc::grid_dep_wait();
         const int quarter = warp & 3;                  // TMEM lanes 32 q .. 32 q + 31
         const int c = quarter * 32 + lane;             // this thread's channel of the tile
-        if (!tc::mbar_wait(tc::smem_u32(&acc_full), 0)) {
-            if (status) atomicOr(status, tc::kTimeoutEpilogue);
-            atomicExch(&failed, 1);
+        const int tokens = min(MC, M - m0);
+        const int n = n0 + c;
+        // the scales come in while the MMAs run
+        const float sw = splits == 1 && n < N ? w_scale[n] : 0.0f;
+        for (int j = lane; j < MC; j += 32)
+            sx_s[warp - 2][j] = splits == 1 && j < tokens ? x_scale[m0 + j] : 0.0f;
+        __syncwarp();
+        if (!tc::mbar_wait_warp(tc::smem_u32(&acc_full), 0)) {
+            give_up(status, tc::kTimeoutEpilogue, &failed);
         } else {
             tc::tc_fence_after();
             const uint32_t src = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-            const int tokens = min(MC, M - m0);
-            const int n = n0 + c;
-            const float sw = splits == 1 && n < N ? w_scale[n] : 0.0f;
             constexpr int kLd = MC < 32 ? 16 : 32;
+            // (rolled: unrolled, 128 tokens took 6100 cycles against 2000,
+            // since each CTA waits for the code of every pass)
 #pragma unroll 1
             for (int c0 = 0; c0 < tokens; c0 += kLd) {
                 uint32_t r[kLd];
@@ -191,29 +276,36 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
 #pragma unroll
                     for (int j = 0; j < kLd; ++j)
                         part[(c0 + j) * kRows + c] = static_cast<int>(r[j]);
-                } else if (n < N) {
+                } else {
+                    YT* dst = y + static_cast<int64_t>(m0 + c0) * N + n;
+                    float v[kLd];
 #pragma unroll
-                    for (int j = 0; j < kLd; ++j)
-                        if (c0 + j < tokens)
-                            store1(y + static_cast<int64_t>(m0 + c0 + j) * N + n,
-                                   scaled(static_cast<int>(r[j]), x_scale[m0 + c0 + j], sw));
+                    for (int j = 0; j < kLd; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&sx_s[warp - 2][c0 + j]);
+                        v[j] = scaled(static_cast<int>(r[j]), f.x, sw);
+                        v[j + 1] = scaled(static_cast<int>(r[j + 1]), f.y, sw);
+                        v[j + 2] = scaled(static_cast<int>(r[j + 2]), f.z, sw);
+                        v[j + 3] = scaled(static_cast<int>(r[j + 3]), f.w, sw);
+                    }
+                    if (n < N) {
+                        const int left = tokens - c0;
+#pragma unroll
+                        for (int j = 0; j < kLd; ++j, dst += N)
+                            if (j < left) store1(dst, v[j]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
     }
 
-    if (warp < 2 && lane != 0) tc::grid_dep_wait();
     __syncthreads();
     __syncwarp();
     if (splits > 1) {
         // every CTA adds its share of the tokens over the cluster's partials
         tc::cluster_sync();
         const int tokens = min(MC, M - m0);
-        uint32_t peer[kMaxSplits];
-#pragma unroll
-        for (int p = 0; p < kMaxSplits; ++p)
-            peer[p] = p < splits ? tc::map_shared_rank(base, static_cast<uint32_t>(p)) : 0;
+        const uint32_t peer0 = tc::map_shared_rank(base, 0);
         const bool wide = (N & 3) == 0;
         // wide: channels 4 lane .. 4 lane + 3 of the tile
         float sw[4];
@@ -223,21 +315,22 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
             sw[j] = n < N ? w_scale[n] : 0.0f;
         }
         const int n = n0 + 4 * lane;
+        // (short code: each of these CTAs runs it a few times only, and what
+        // it costs first is its instructions' way from memory)
 #pragma unroll 1
         for (int m = rank + splits * warp; m < tokens; m += splits * (kThreads / 32)) {
-            const uint32_t off = static_cast<uint32_t>((m * kRows + 4 * lane) * 4);
-            int4 v[kMaxSplits];
-#pragma unroll
-            for (int p = 0; p < kMaxSplits; ++p)
-                if (p < splits) v[p] = tc::ld_cluster_i4(peer[p] + off);
-            int4 t = make_int4(0, 0, 0, 0);
-#pragma unroll
-            for (int p = 0; p < kMaxSplits; ++p) {
-                if (p < splits) {
-                    t.x += v[p].x; t.y += v[p].y; t.z += v[p].z; t.w += v[p].w;
-                }
-            }
             const float sx = x_scale[m0 + m];
+            const uint32_t off = static_cast<uint32_t>((m * kRows + 4 * lane) * 4);
+            int4 t = tc::ld_cluster_i4(peer0 + off);
+            int4 v[kMaxSplits - 1];
+#pragma unroll
+            for (int p = 1; p < kMaxSplits; ++p)
+                v[p - 1] = p < splits ? tc::ld_cluster_i4(tc::map_shared_rank(base + off, p))
+                                      : make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int p = 0; p < kMaxSplits - 1; ++p) {
+                t.x += v[p].x; t.y += v[p].y; t.z += v[p].z; t.w += v[p].w;
+            }
             const float o[4] = {scaled(t.x, sx, sw[0]), scaled(t.y, sx, sw[1]),
                                 scaled(t.z, sx, sw[2]), scaled(t.w, sx, sw[3])};
             YT* dst = y + static_cast<int64_t>(m0 + m) * N + n;
@@ -273,36 +366,48 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
 //              bytes); both CTAs' loads complete on it
 //   empty[s]   both: the leader's commit of the stage
 //   acc_full   both: the leader's commit of the tile
-//   acc_empty  leader: the four epilogue warps of both CTAs
-constexpr int kPairStages = 6;
-constexpr uint32_t kPairHalf = 128 * kBK;
-constexpr uint32_t kPairStage = 2 * kPairHalf;
-constexpr size_t kPairDynamic = static_cast<size_t>(kPairStage) * kPairStages + 1024;
+//   acc_empty  leader: the eight epilogue warps of both CTAs
+constexpr int kPairThreads = 64 + 8 * 32;             // two epilogue warps a TMEM lane quarter
+template <int TN>
+struct PairSmem {
+    static constexpr int kAtoms = TN == 256 ? 1 : 2;     // of K a stage
+    static constexpr uint32_t kX = 128 * kAtom;          // a CTA's half of the tokens, one atom
+    static constexpr uint32_t kW = TN / 2 * kAtom;       // and of the channels
+    static constexpr uint32_t kStage = kAtoms * (kX + kW);
+    static constexpr int kStages = 196608 / kStage;
+    static constexpr uint32_t kRing = kStage * kStages;
+    static constexpr size_t kDynamic = kRing + 1024;
+};
 
-template <typename YT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int TN, typename YT>
+__global__ void __launch_bounds__(kPairThreads, 1)
 linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
                       const __grid_constant__ CUtensorMap tmap_w,
                       const float* __restrict__ x_scale, const float* __restrict__ w_scale,
-                      YT* __restrict__ y, int M, int N, int K, uint32_t* __restrict__ status) {
+                      YT* __restrict__ y, bool wide, int M, int N, int K,
+                      uint32_t* __restrict__ status) {
+    using L = PairSmem<TN>;
+    constexpr int kPairStages = L::kStages;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kPairStages];
     __shared__ __align__(8) uint64_t empty[kPairStages];
     __shared__ __align__(8) uint64_t acc_full[2];
     __shared__ __align__(8) uint64_t acc_empty[2];
     __shared__ uint32_t tmem_slot;
+    __shared__ __align__(16) float sw_s[8][TN / 2];    // the scales of a warp's channels
     __shared__ int issued, consumed;
     __shared__ int failed;
 
     const uint32_t raw = tc::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const int warp = threadIdx.x >> 5;
+    const int warp = tc::warp_index();
     const int lane = threadIdx.x & 31;
     const int rank = static_cast<int>(tc::cluster_ctarank());   // 0: leader
     const int pair = static_cast<int>(blockIdx.x >> 1);
     const int n_pairs = static_cast<int>(gridDim.x >> 1);
+    constexpr int kBK = L::kAtoms * kAtom;
     const int n_kt = (K + kBK - 1) / kBK;
-    const int tiles_n = (N + 255) / 256;
+    const int tiles_n = (N + TN - 1) / TN;
     const int n_tiles = tiles_n * ((M + 255) / 256);
 
     if (threadIdx.x == 0) {
@@ -312,7 +417,7 @@ linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
         }
         for (int a = 0; a < 2; ++a) {
             tc::mbar_init(tc::smem_u32(&acc_full[a]), 1);
-            tc::mbar_init(tc::smem_u32(&acc_empty[a]), 8);
+            tc::mbar_init(tc::smem_u32(&acc_empty[a]), 16);
         }
         tc::fence_mbar_init();
         issued = 0;
@@ -320,7 +425,7 @@ linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
         failed = 0;
     }
     if (warp == 1) {
-        tc::tmem_alloc_pair(tc::smem_u32(&tmem_slot), 512);
+        tc::tmem_alloc_pair(tc::smem_u32(&tmem_slot), 2 * TN);
         tc::tmem_relinquish_pair();
     }
     // both CTAs' barriers exist before either signals the other's
@@ -332,110 +437,153 @@ linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
     const uint32_t tmem = tmem_slot;
     volatile int* vfailed = &failed;
     tc::grid_dep_launch();
+    int done = 0;                                      // k-steps issued, or consumed
 
-    if (warp == 0 && lane == 0) {
-        tc::prefetch_tmap(&tmap_x);
-        tc::prefetch_tmap(&tmap_w);
+    if (warp == 0) {
+        if (tc::elect_one()) {
+            tc::prefetch_tmap(&tmap_x);
+            tc::prefetch_tmap(&tmap_w);
+        }
         tc::grid_dep_wait();
-        int s = 0, g = 0;
+        const uint32_t full0 = tc::map_shared_rank(tc::smem_u32(&full[0]), 0);   // the leader's
+        int s = 0;
         uint32_t ph = 1;
-        for (int tile = pair; tile < n_tiles && !*vfailed; tile += n_pairs) {
+        bool ready = true;
+        for (int tile = pair; tile < n_tiles && !__any_sync(kFull, *vfailed); tile += n_pairs) {
             const int m0 = (tile / tiles_n) * 256 + rank * 128;
-            const int n0 = (tile % tiles_n) * 256 + rank * 128;
+            const int n0 = (tile % tiles_n) * TN + rank * (TN / 2);
             for (int kt = 0; kt < n_kt; ++kt) {
-                if (!tc::mbar_wait(tc::smem_u32(&empty[s]), ph)) {
-                    if (status) atomicOr(status, tc::kTimeoutProducer);
-                    atomicExch(&failed, 1);
+                if (!__all_sync(kFull, ready) && !tc::mbar_wait_warp(tc::smem_u32(&empty[s]), ph)) {
+                    give_up(status, tc::kTimeoutProducer, &failed);
                     break;
                 }
-                const uint32_t a = base + s * kPairStage;
-                const uint32_t fb = tc::map_shared_rank(tc::smem_u32(&full[s]), 0);
-                if (rank == 0) tc::mbar_arrive_expect_tx(tc::smem_u32(&full[s]), 2 * kPairStage);
-                tc::tma_load_2d_pair(a, &tmap_w, fb, kt * kBK, n0);
-                tc::tma_load_2d_pair(a + kPairHalf, &tmap_x, fb, kt * kBK, m0);
-                issued = ++g;
+                const uint32_t a = base + s * L::kStage;
+                const uint32_t fb = full0 + 8 * s;
+                const uint32_t own = tc::smem_u32(&full[s]);
                 if (++s == kPairStages) { s = 0; ph ^= 1; }
+                ready = tc::mbar_test_wait(tc::smem_u32(&empty[s]), ph);   // for the next pass
+                if (tc::elect_one()) {
+                    if (rank == 0) tc::mbar_arrive_expect_tx(own, 2 * L::kStage);
+#pragma unroll
+                    for (int i = 0; i < L::kAtoms; ++i) {
+                        const int k0 = kt * kBK + i * kAtom;
+                        tc::tma_load_2d_pair(a + i * L::kX, &tmap_x, fb, k0, m0);
+                        tc::tma_load_2d_pair(a + L::kAtoms * L::kX + i * L::kW, &tmap_w, fb, k0, n0);
+                    }
+                }
+                ++done;
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+        if (lane == 0) issued = done;
+    } else if (warp == 1 && rank == 0) {
         tc::grid_dep_wait();
-        const uint32_t idesc = tc::idesc_s8_s32(256, 256);
-        int s = 0, g = 0;
+        const uint32_t idesc = tc::idesc_s8_s32(256, TN);
+        int s = 0;
         uint32_t ph = 0;
+        bool ready = false;
         bool ok = true;
         int li = 0;
         for (int tile = pair; ok && tile < n_tiles; tile += n_pairs, ++li) {
             const int acc = li & 1;
-            const uint32_t d = tmem + static_cast<uint32_t>(acc) * 256;
-            if (!tc::mbar_wait(tc::smem_u32(&acc_empty[acc]), ((li >> 1) & 1) ^ 1)) {
-                if (status) atomicOr(status, tc::kTimeoutMma);
-                atomicExch(&failed, 1);
+            const uint32_t d = tmem + static_cast<uint32_t>(acc) * TN;
+            if (!tc::mbar_wait_warp(tc::smem_u32(&acc_empty[acc]), ((li >> 1) & 1) ^ 1)) {
+                give_up(status, tc::kTimeoutMma, &failed);
                 break;
             }
             tc::tc_fence_after();
             for (int kt = 0; kt < n_kt; ++kt) {
-                if (!tc::mbar_wait(tc::smem_u32(&full[s]), ph)) {
-                    if (status) atomicOr(status, tc::kTimeoutMma);
-                    atomicExch(&failed, 1);
+                if (!__all_sync(kFull, ready) && !tc::mbar_wait_warp(tc::smem_u32(&full[s]), ph)) {
+                    give_up(status, tc::kTimeoutMma, &failed);
                     ok = false;
                     break;
                 }
-                consumed = ++g;
                 tc::tc_fence_after();
-                const uint64_t a = tc::desc_k_sw128(base + s * kPairStage);
-                const uint64_t b = tc::desc_k_sw128(base + s * kPairStage + kPairHalf);
-#pragma unroll
-                for (int kk = 0; kk < kBK / 32; ++kk)
-                    tc::mma_i8_pair(d, a + 2 * kk, b + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
-                tc::mma_commit_pair(tc::smem_u32(&empty[s]), 0x3);
+                const uint64_t a = tc::desc_k_sw128(base + s * L::kStage);
+                const uint64_t b = tc::desc_k_sw128(base + s * L::kStage + L::kAtoms * L::kX);
+                const uint32_t eb = tc::smem_u32(&empty[s]);
                 if (++s == kPairStages) { s = 0; ph ^= 1; }
+                ready = tc::mbar_test_wait(tc::smem_u32(&full[s]), ph);
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 32; ++kk) {
+                        const int i = kk / 4, o = 2 * (kk % 4);
+                        tc::mma_i8_pair(d, a + (i * L::kX >> 4) + o, b + (i * L::kW >> 4) + o, idesc,
+                                        (kt > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    tc::mma_commit_pair(eb, 0x3);
+                    if (kt == n_kt - 1) tc::mma_commit_pair(tc::smem_u32(&acc_full[acc]), 0x3);
+                }
+                ++done;
             }
-            if (ok) tc::mma_commit_pair(tc::smem_u32(&acc_full[acc]), 0x3);
         }
+        if (lane == 0) consumed = done;
     } else if (warp >= 2) {
         tc::grid_dep_wait();
-        const int quarter = warp & 3;
+        const int quarter = warp & 3;                  // TMEM lanes 32 q .. 32 q + 31
+        const int col0 = (warp - 2) / 4 * (TN / 2);    // and half of the tile's channels
         const uint32_t ae0 = tc::map_shared_rank(tc::smem_u32(&acc_empty[0]), 0);
         const uint32_t ae1 = tc::map_shared_rank(tc::smem_u32(&acc_empty[1]), 0);
         int li = 0;
         for (int tile = pair; tile < n_tiles; tile += n_pairs, ++li) {
             const int acc = li & 1;
-            if (!tc::mbar_wait(tc::smem_u32(&acc_full[acc]), (li >> 1) & 1)) {
-                if (status) atomicOr(status, tc::kTimeoutEpilogue);
-                atomicExch(&failed, 1);
+            const int row = (tile / tiles_n) * 256 + rank * 128 + quarter * 32 + lane;   // token
+            const int n0 = (tile % tiles_n) * TN + col0;
+            const int channels = min(TN / 2, N - n0);  // 0 or less: nothing but the hand-over
+            const float sx = row < M ? x_scale[row] : 0.0f;
+            float* sws = sw_s[warp - 2];
+#pragma unroll
+            for (int j = 0; j < TN / 2; j += 32)
+                sws[j + lane] = j + lane < channels ? w_scale[n0 + j + lane] : 0.0f;
+            const uint32_t src = tmem + static_cast<uint32_t>(acc) * TN + col0 +
+                                 (static_cast<uint32_t>(quarter * 32) << 16);
+            if (!tc::mbar_wait_warp(tc::smem_u32(&acc_full[acc]), (li >> 1) & 1)) {
+                give_up(status, tc::kTimeoutEpilogue, &failed);
                 break;
             }
             tc::tc_fence_after();
-            const int m0 = (tile / tiles_n) * 256;
-            const int n = (tile % tiles_n) * 256 + rank * 128 + quarter * 32 + lane;
-            const int tokens = min(256, M - m0);
-            const float sw = n < N ? w_scale[n] : 0.0f;
-            const uint32_t src = tmem + static_cast<uint32_t>(acc) * 256 +
-                                 (static_cast<uint32_t>(quarter * 32) << 16);
+            if (channels <= 0 && lane == 0) tc::mbar_arrive_cluster_local(acc ? ae1 : ae0);
 #pragma unroll 1
-            for (int c0 = 0; c0 < tokens; c0 += 32) {
+            for (int c0 = 0; c0 < channels; c0 += 32) {
                 uint32_t r[32];
                 tc::tmem_ld_32x32b_x32(src + c0, r);
                 tc::tmem_ld_wait();
-                if (n < N) {
-                    YT* dst = y + static_cast<int64_t>(m0 + c0) * N + n;
+                if (c0 + 32 >= channels) {        // every read of this set is done: hand it back
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster_local(acc ? ae1 : ae0);
+                }
+                float v[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j, dst += N)
-                        if (c0 + j < tokens)
-                            store1(dst, scaled(static_cast<int>(r[j]), x_scale[m0 + c0 + j], sw));
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(sws + c0 + j);
+                    v[j] = scaled(static_cast<int>(r[j]), sx, f.x);
+                    v[j + 1] = scaled(static_cast<int>(r[j + 1]), sx, f.y);
+                    v[j + 2] = scaled(static_cast<int>(r[j + 2]), sx, f.z);
+                    v[j + 3] = scaled(static_cast<int>(r[j + 3]), sx, f.w);
+                }
+                if (wide) {
+                    if (row < M)
+                        store32(y + static_cast<int64_t>(row) * N + n0 + c0, v, channels - c0);
+                } else {
+                    // rows that are not aligned: one token's 32 channels a store
+                    transpose32(v, lane);
+                    YT* col = y + static_cast<int64_t>(row - lane) * N + n0 + c0 + lane;
+                    if (lane < channels - c0) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (row - lane + j < M) store1(col + static_cast<int64_t>(j) * N, v[j]);
+                    }
                 }
                 __syncwarp();
             }
-            tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(acc ? ae1 : ae0);   // the leader's set is free
         }
     }
 
     // Both CTAs meet here; then the leader lets copies still addressed to its
     // barriers land (after a timeout only), and both meet again before TMEM
     // and shared memory are released.
-    if (warp < 2 && (lane != 0 || (warp == 1 && rank != 0))) tc::grid_dep_wait();
+    if (warp == 1 && rank != 0) tc::grid_dep_wait();
     tc::tc_fence_before();
     __syncthreads();
     __syncwarp();
@@ -449,7 +597,102 @@ linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
     __syncwarp();
     tc::cluster_sync();
     tc::tc_fence_after();
-    if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
+    if (warp == 1) tc::tmem_dealloc_pair(tmem, 2 * TN);
+}
+
+// ---- few tokens --------------------------------------------------------------------
+// The weights are read once and everything else is small: a warp reads R rows
+// of w in 16-byte pieces, multiplies them with MT tokens' bytes four at a time
+// and adds over its lanes. Nothing is shared between warps, so there is no
+// barrier, and the weights of every warp are on their way at once.
+constexpr int kVecThreads = 128;
+
+__device__ __forceinline__ int4 ld_stream_i4(const int8_t* p) {
+    int4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+template <int MT, int R, int W, typename YT>
+__global__ void __launch_bounds__(kVecThreads)
+linear_i8_vec_kernel(const int8_t* __restrict__ x, const float* __restrict__ x_scale,
+                     const int8_t* __restrict__ w, const float* __restrict__ w_scale,
+                     YT* __restrict__ y, int M, int N, int K) {
+    constexpr int kWarps = kVecThreads / 32;
+    constexpr int U = 2;                               // pieces of a row in flight
+    constexpr int kSpan = 512 * W;                     // bytes that W warps read at once
+    static_assert(MT * R <= 32, "a lane for each sum");
+    __shared__ int part[W > 1 ? kWarps : 1][MT * R];
+    const int lane = threadIdx.x & 31;
+    const int warp = tc::warp_index();
+    const int n0 = (static_cast<int>(blockIdx.x) * (kWarps / W) + warp / W) * R;
+    const int m0 = static_cast<int>(blockIdx.y) * MT;
+    const int at = warp % W * 32 + lane;               // this thread's place in a row
+    tc::grid_dep_launch();
+    const int8_t* wr[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) wr[r] = w + static_cast<int64_t>(min(n0 + r, N - 1)) * K;
+    // the weights head for L2 while the previous kernel ends
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (at * 128 < K) asm volatile("prefetch.global.L2 [%0];" ::"l"(wr[r] + at * 128));
+    tc::grid_dep_wait();
+    const int8_t* xr[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xr[m] = x + static_cast<int64_t>(min(m0 + m, M - 1)) * K;
+    int acc[MT][R] = {};
+    // `pieces` pieces of 16 bytes a thread, all loads first
+    auto step = [&](int k, auto pieces) {
+        constexpr int P = decltype(pieces)::value;
+        int4 wv[P][R], xv[P][MT];
+#pragma unroll
+        for (int u = 0; u < P; ++u) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) wv[u][r] = ld_stream_i4(wr[r] + k + kSpan * u);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                xv[u][m] = __ldg(reinterpret_cast<const int4*>(xr[m] + k + kSpan * u));
+        }
+#pragma unroll
+        for (int u = 0; u < P; ++u) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    acc[m][r] = __dp4a(wv[u][r].x, xv[u][m].x, acc[m][r]);
+                    acc[m][r] = __dp4a(wv[u][r].y, xv[u][m].y, acc[m][r]);
+                    acc[m][r] = __dp4a(wv[u][r].z, xv[u][m].z, acc[m][r]);
+                    acc[m][r] = __dp4a(wv[u][r].w, xv[u][m].w, acc[m][r]);
+                }
+            }
+        }
+    };
+    int k = at * 16;
+    for (; k + kSpan * (U - 1) < K; k += kSpan * U) step(k, std::integral_constant<int, U>{});
+    for (; k < K; k += kSpan) step(k, std::integral_constant<int, 1>{});
+    // lane m R + r keeps the sum of token m0 + m and channel n0 + r
+    int mine = 0;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = __reduce_add_sync(kFull, acc[m][r]);
+            if (lane == m * R + r) mine = t;
+        }
+    }
+    if constexpr (W > 1) {
+        if (lane < MT * R) part[warp][lane] = mine;
+        __syncthreads();
+        if (warp % W != 0) return;
+        if (lane < MT * R) {
+#pragma unroll
+            for (int i = 1; i < W; ++i) mine += part[warp + i][lane];
+        }
+    }
+    const int m = m0 + lane / R, n = n0 + lane % R;
+    if (lane < MT * R && m < M && n < N)
+        store1(y + static_cast<int64_t>(m) * N + n, scaled(mine, x_scale[m], w_scale[n]));
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -459,7 +702,7 @@ bool make_tmap_i8(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, in
     if (!fn) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kAtom), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estr[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -481,11 +724,11 @@ cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<bool> (&don
     return err;
 }
 
-cudaLaunchConfig_t cluster_config(unsigned grid, int cluster, size_t smem, cudaStream_t stream,
-                                  cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t cluster_config(unsigned grid, int threads, int cluster, size_t smem,
+                                  cudaStream_t stream, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -512,49 +755,149 @@ cudaError_t launch_split(const LinearI8Args& a, int splits, cudaStream_t stream)
     const int64_t ctas = ((a.N + kRows - 1) / kRows) * ((a.M + MC - 1) / MC) * splits;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = cluster_config(static_cast<unsigned>(ctas), splits,
+    const cudaLaunchConfig_t cfg = cluster_config(static_cast<unsigned>(ctas), kThreads, splits,
                                                   SplitSmem<MC>::kDynamic, stream, attr);
     return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a.x_scale, a.w_scale, static_cast<YT*>(a.y),
                               static_cast<int>(a.M), static_cast<int>(a.N),
                               static_cast<int>(a.K), splits, a.status);
 }
 
-template <typename YT>
+template <int TN, typename YT>
 cudaError_t launch_pair(const LinearI8Args& a, cudaStream_t stream) {
     static std::atomic<bool> done[kDevs];
-    const auto kernel = linear_i8_pair_kernel<YT>;
-    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), kPairDynamic, done);
+    const auto kernel = linear_i8_pair_kernel<TN, YT>;
+    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), PairSmem<TN>::kDynamic, done);
     if (err != cudaSuccess) return err;
     CUtensorMap tx, tw;
-    if (!make_tmap_i8(&tx, a.x, a.M, a.K, 128) || !make_tmap_i8(&tw, a.w, a.N, a.K, 128))
+    if (!make_tmap_i8(&tx, a.x, a.M, a.K, 128) || !make_tmap_i8(&tw, a.w, a.N, a.K, TN / 2))
         return cudaErrorInvalidValue;
-    const int64_t tiles = ((a.N + 255) / 256) * ((a.M + 255) / 256);
+    const int64_t tiles = ((a.N + TN - 1) / TN) * ((a.M + 255) / 256);
     if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
     const int64_t pairs = std::min<int64_t>(tiles, device_sm_count() / 2);
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg =
-        cluster_config(static_cast<unsigned>(2 * pairs), 2, kPairDynamic, stream, attr);
-    return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a.x_scale, a.w_scale, static_cast<YT*>(a.y),
-                              static_cast<int>(a.M), static_cast<int>(a.N),
-                              static_cast<int>(a.K), a.status);
+    const cudaLaunchConfig_t cfg = cluster_config(static_cast<unsigned>(2 * pairs), kPairThreads, 2,
+                                                  PairSmem<TN>::kDynamic, stream, attr);
+    return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a.x_scale, a.w_scale,
+                              static_cast<YT*>(a.y),
+                              ((a.N * sizeof(YT)) | reinterpret_cast<uintptr_t>(a.y)) % 32 == 0, static_cast<int>(a.M),
+                              static_cast<int>(a.N), static_cast<int>(a.K), a.status);
+}
+
+template <int MT, int R, int W, typename YT>
+cudaError_t launch_vec_r(const LinearI8Args& a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    const int64_t rows = kVecThreads / 32 / W * R;
+    cfg.gridDim = dim3(static_cast<unsigned>((a.N + rows - 1) / rows),
+                       static_cast<unsigned>((a.M + MT - 1) / MT));
+    cfg.blockDim = dim3(kVecThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, linear_i8_vec_kernel<MT, R, W, YT>, a.x, a.x_scale, a.w,
+                              a.w_scale, static_cast<YT*>(a.y), static_cast<int>(a.M),
+                              static_cast<int>(a.N), static_cast<int>(a.K));
+}
+
+// W warps share a row so that long rows are on their way at once: at one
+// token 2048 x 4096 takes 2.7 with 4, 2.8 with 2 and 3.7 with one,
+// 4096 x 2048 3.0 (R = 4: 2.5), 2.6 and 3.1, 2048 x 512 1.7, 1.6 and 1.5.
+int vec_warps(int64_t K) { return K >= 4096 ? 4 : K >= 1024 ? 2 : 1; }
+
+template <int MT, int R, typename YT>
+cudaError_t launch_vec_w(const LinearI8Args& a, cudaStream_t stream) {
+    switch (vec_warps(a.K)) {
+        case 4: return launch_vec_r<MT, R, 4, YT>(a, stream);
+        case 2: return launch_vec_r<MT, R, 2, YT>(a, stream);
+        default: return launch_vec_r<MT, R, 1, YT>(a, stream);
+    }
+}
+
+// R rows a warp: as many as keep its loads few without leaving it too few in
+// flight (8 x 2048 x 4096: 4.1 with 4 against 4.3 with 2; 8 x 4096 x 2048:
+// 4.4 with 2; 1 x 1000 x 10000: 3.7 with 2, 5.2 with 4).
+template <typename YT>
+cudaError_t launch_vec(const LinearI8Args& a, cudaStream_t stream) {
+    if (a.M <= 1) return launch_vec_w<1, 2, YT>(a, stream);
+    if (a.M <= 2) return launch_vec_w<2, 2, YT>(a, stream);
+    if (a.M <= 4) return launch_vec_w<4, 4, YT>(a, stream);
+    if (vec_warps(a.K) == 4) return launch_vec_r<8, 4, 4, YT>(a, stream);
+    if (vec_warps(a.K) == 2) return launch_vec_r<8, 2, 2, YT>(a, stream);
+    return launch_vec_r<8, 2, 1, YT>(a, stream);
+}
+
+// Which kernel takes a product.
+struct PlanI8 {
+    enum Form { kVec, kSplit, kPair } form;
+    int tile;      // split: tokens a tile; pair: channels a tile
+    int splits;    // split: CTAs of a cluster
+};
+
+// The form with the least device time by a model of it (microseconds, graph
+// replays on a B200, fitted to 50 shapes between 1 x 64 x 2048 and
+// 16384 x 8192 x 2048; sums are exact, so the choice never shows in a result).
+//   vec    a wave of warps (16 an SM) takes 0.4 + 0.39 per 1000 bytes of its
+//          rows, after 1.1: 256 x 64 x 2048 in 2.8 against 3.6 (split), but
+//          64 x 1024 x 1024 in 3.6 against 3.1. Calls of at most 4 tokens
+//          always: 1 x 8192 x 2048 in 4.0 against 5.5.
+//   split  a wave of CTAs starts and ends in 1.75 .. 2.9 and spends 0.27 ..
+//          0.5 on 256 bytes of K; adding over a cluster costs 1.6 .. 2.9 more:
+//          16 x 256 x 8192 in 4.6 with 8 CTAs against 10 with one, but
+//          64 x 4096 x 2048 in 6.0 with 4 against 5.0 with one.
+//   pair   starts and ends once, 4.9 or 5.6, and overlaps its tiles:
+//          1024 x 8192 x 2048 in 18.2 against 29.5 (split), but
+//          256 x 4096 x 2048 in 7.7 against 5.7.
+PlanI8 plan_i8(int64_t M, int64_t N, int64_t K) {
+    if (M <= 4) return {PlanI8::kVec, 0, 0};
+    const int64_t sms = device_sm_count();
+    const auto waves = [](int64_t n, int64_t at_once) {
+        return static_cast<float>((n + at_once - 1) / at_once);
+    };
+    const float steps = waves(K, 256);
+    PlanI8 best = {PlanI8::kVec, 0, 0};
+    const int w = vec_warps(K), r = w == 4 ? 4 : 2;
+    float least = 1.1f + waves((M + 7) / 8 * ((N + r - 1) / r) * w, 16 * sms) *
+                             (0.4f + 0.00039f * K * r / w);
+    const auto consider = [&](float t, PlanI8 p) {
+        if (t < least) { least = t; best = p; }
+    };
+    struct { int tokens; float ends, step; } const tiles[] = {
+        {16, 1.75f, 0.275f}, {32, 1.9f, 0.29f}, {64, 2.25f, 0.42f}, {128, 2.9f, 0.5f}};
+    for (const auto& t : tiles) {
+        if (t.tokens > 16 && t.tokens >= 2 * M) break;
+        const int64_t n = ((N + kRows - 1) / kRows) * ((M + t.tokens - 1) / t.tokens);
+        consider(waves(n, sms) * (t.ends + steps * t.step), {PlanI8::kSplit, t.tokens, 1});
+        // (clusters of 8 find room for 96 CTAs at once at most)
+        for (const int s : {2, 4, 8}) {
+            if (s > steps || n * s > (s == 8 ? 96 : sms)) break;
+            consider(t.ends + waves(static_cast<int64_t>(steps), s) * t.step + 1.4f +
+                         0.012f * t.tokens,
+                     {PlanI8::kSplit, t.tokens, s});
+        }
+    }
+    if (M > 128) {
+        const int64_t rows = (M + 255) / 256;
+        const float w1 = waves(rows * ((N + 127) / 128), sms / 2);
+        const float w2 = waves(rows * ((N + 255) / 256), sms / 2);
+        consider(4.1f + w1 * (0.8f + 0.39f * steps), {PlanI8::kPair, 128, 1});
+        consider(5.1f + w2 * (0.5f + 0.72f * steps), {PlanI8::kPair, 256, 1});
+    }
+    return best;
 }
 
 template <typename YT>
 cudaError_t launch_typed(const LinearI8Args& a, cudaStream_t stream) {
-    const int64_t sms = device_sm_count();
-    const int64_t n_kt = (a.K + kBK - 1) / kBK;
-    const int64_t pair_tiles = ((a.N + 255) / 256) * ((a.M + 255) / 256);
-    if (pair_tiles >= sms / 2) return launch_pair<YT>(a, stream);
-    int mc = 16;
-    while (mc < 128 && mc < a.M) mc *= 2;
-    const int64_t tiles = ((a.N + kRows - 1) / kRows) * ((a.M + mc - 1) / mc);
-    const int splits = static_cast<int>(
-        std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, n_kt, sms / tiles})));
-    switch (mc) {
-        case 16: return launch_split<16, YT>(a, splits, stream);
-        case 32: return launch_split<32, YT>(a, splits, stream);
-        case 64: return launch_split<64, YT>(a, splits, stream);
-        default: return launch_split<128, YT>(a, splits, stream);
+    const PlanI8 p = plan_i8(a.M, a.N, a.K);
+    if (p.form == PlanI8::kVec) return launch_vec<YT>(a, stream);
+    if (p.form == PlanI8::kPair)
+        return p.tile == 256 ? launch_pair<256, YT>(a, stream) : launch_pair<128, YT>(a, stream);
+    switch (p.tile) {
+        case 16: return launch_split<16, YT>(a, p.splits, stream);
+        case 32: return launch_split<32, YT>(a, p.splits, stream);
+        case 64: return launch_split<64, YT>(a, p.splits, stream);
+        default: return launch_split<128, YT>(a, p.splits, stream);
     }
 }
 

@@ -35,6 +35,23 @@ __device__ __forceinline__ uint64_t global_timer() {
     return t;
 }
 
+// True in one lane of a converged warp. Copies and MMAs issued under it, in a
+// loop that the whole warp runs, take their operands through uniform registers;
+// under a test of the lane number the compiler has to serialise every issue
+// (a k-step of two tile loads: 253 cycles against 411).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "elect.sync _|P, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// The warp's number, known to be the same in all its lanes.
+__device__ __forceinline__ int warp_index() {
+    return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+}
+
 // ---- mbarrier --------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -60,6 +77,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// The same without waiting at all.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // Wait for the phase with the given parity to complete; false once
 // `limit_ns` of %globaltimer have passed without it. The timer is read once
 // per kPollsPerCheck polls, so that reading it does not delay noticing the
@@ -75,6 +104,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
             if (mbar_try_wait(bar, parity)) return true;
         if (global_timer() - t0 > limit_ns) return false;
     }
+}
+
+// The same by a whole converged warp, whose lanes all get one answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
 // ---- TMA: 2D tiled load global -> shared, completing on an mbarrier --------
@@ -277,6 +311,11 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t cta_mask)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
                  ::"r"(bar_cluster) : "memory");
+}
+// The same without ordering the thread's global stores (release at cluster
+// scope waits for them to drain): for handing back TMEM that has been read.
+__device__ __forceinline__ void mbar_arrive_cluster_local(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 // ---- thread-block clusters: rank, barrier, distributed shared memory -------
