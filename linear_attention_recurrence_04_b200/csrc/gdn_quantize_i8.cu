@@ -13,8 +13,8 @@
 // summed. h is rounded to the residual's type before the norm reads it,
 // because that is the row the next layer reads back.
 //
-// The integers are decided exactly: t = a * fp32(127 / m) is within 1.6e-5 of
-// 127 a / m, and where t lies closer than 2^-15 to a half the side is taken
+// The integers are decided exactly: a * fp32(127 / m) is within 2^-17 of
+// 127 a / m, and where it lies closer than 2^-16 to a half the side is taken
 // from the sign of 254 |a| - (2 floor|t| + 1) m, whose two products are exact
 // in double. The squares are summed in double: no row of finite values
 // overflows, and the scale is rounded to fp32 once.
@@ -31,34 +31,50 @@ namespace gdn {
 namespace {
 
 constexpr int kVec = 8;              // elements a thread moves at once
-constexpr int kMaxThreads = 1024;    // threads of a row
-constexpr int kMaxGroups = 4;        // groups of kVec a thread keeps in registers
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[kVec]) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    const float4 b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[kVec]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+// Eight elements as they come from memory.
+template <typename T>
+struct Raw {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            v[i] = reinterpret_cast<const uint4*>(p)[i];
     }
-}
+    __device__ __forceinline__ void unpack(float (&f)[kVec]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f[4 * i] = __uint_as_float(v[i].x);
+                f[4 * i + 1] = __uint_as_float(v[i].y);
+                f[4 * i + 2] = __uint_as_float(v[i].z);
+                f[4 * i + 3] = __uint_as_float(v[i].w);
+            }
+        } else {
+            const uint32_t u[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(u[i] << 16);
+                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+        }
+    }
+};
 __device__ __forceinline__ void round_to(float*, float (&)[kVec]) {}
 __device__ __forceinline__ void round_to(__nv_bfloat16*, float (&v)[kVec]) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = __bfloat162float(__float2bfloat16_rn(v[i]));
+    for (int i = 0; i < kVec; i += 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[i], v[i + 1]);
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+        v[i] = __uint_as_float(u << 16);
+        v[i + 1] = __uint_as_float(u & 0xffff0000u);
+    }
 }
 __device__ __forceinline__ void store8(float* p, const float (&v)[kVec]) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
-// (the values are bf16 already: their low halves are zero, or they are NaN)
+// (the values are bf16 already: their low halves are zero)
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[kVec]) {
     uint32_t u[4];
 #pragma unroll
@@ -67,45 +83,96 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[kVec])
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// The row's factors once its maximum is known. Rows whose maximum is below
-// 1e-30 are raised by 2^100 first (exactly), so that 127 / m stays finite.
-struct RowQuant {
-    float up, m, r;
-    bool zero;       // nothing to scale, or a value that is not finite: q = 0
-    __device__ explicit RowQuant(uint32_t mbits) {
-        const float top = __uint_as_float(mbits);
-        zero = mbits == 0u || mbits >= 0x7f800000u;
-        up = top < 1e-30f ? 0x1p100f : 1.0f;
-        m = top * up;
-        r = zero ? 0.0f : __fdiv_rn(127.0f, m);
-    }
-    // 127 a / m to the nearest integer as the low byte.
-    __device__ uint32_t operator()(float a0) const {
-        constexpr float kMagic = 12582912.0f;       // 1.5 * 2^23: the sum's low bits are rint(t)
-        const float a = zero ? 0.0f : a0 * up;
-        const float t = __fmul_rn(a, r);
-        const float s = __fadd_rn(t, kMagic);
-        uint32_t q = __float_as_uint(s);
-        if (fabsf(t - __fadd_rn(s, -kMagic)) > 0.5f - 0x1p-15f) {
-            const float f = floorf(fabsf(t));
-            const double c = 254.0 * static_cast<double>(fabsf(a)) -
-                             static_cast<double>(2.0f * f + 1.0f) * static_cast<double>(m);
-            const int k = static_cast<int>(f);
-            const int n = c > 0.0 ? k + 1 : c < 0.0 ? k : k + (k & 1);
-            q = static_cast<uint32_t>(a < 0.0f ? -n : n);
-        }
-        return q;
-    }
-    __device__ uint2 pack8(const float (&a)[kVec]) const {
-        uint32_t b[kVec];
+// max(top, |a|, |b|), a NaN once any of them is one.
+__device__ __forceinline__ float max_abs(float top, float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(top), "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+
+// Distances from an integer above this are decided exactly.
+constexpr float kNear = 0.5f - 0x1p-16f;
+constexpr float kMagic = 12582912.0f;           // 1.5 * 2^23: a sum's low bits are rint
+
+__device__ __forceinline__ uint2 low_bytes(const uint32_t (&b)[kVec]) {
+    uint2 o;
+    o.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    o.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    return o;
+}
+
+// Eight integers of a row of bf16 values, ri = fp32(1 / m), with no case left
+// over. Halves are common here (254 a = (2 k + 1) m for one value in a few
+// hundred, 8-bit mantissas), so the quotient itself is corrected: p = 127 a
+// has 15 bits, the remainder e = p - t m of its first value is exact, and
+// t + e ri is then off by less than 2^-24 of it. A quotient that is no half
+// is further than 2^-17 of it from one (254 a and (2 k + 1) m differ by a
+// unit of the 16 bits they have), and a half is hit exactly.
+__device__ __forceinline__ uint2 quantize8_bf16(const float (&a)[kVec], float m, float ri) {
+    uint32_t b[kVec];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) b[i] = (*this)(a[i]);
-        uint2 o;
-        o.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-        o.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-        return o;
+    for (int i = 0; i < kVec; ++i) {
+        const float p = __fmul_rn(a[i], 127.0f);
+        const float t = __fmul_rn(p, ri);
+        b[i] = __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-t, m, p), ri, t), kMagic));
     }
-};
+    return low_bytes(b);
+}
+
+// Eight integers of any row, r = fp32(127 / m): a r differs from 127 a / m by
+// less than 2^-17. `far` grows to the largest distance of an a r from its
+// integer.
+__device__ __forceinline__ uint2 quantize8(const float (&a)[kVec], float r, float& far) {
+    uint32_t b[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2) {
+        float d[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float s = __fmaf_rn(a[i + j], r, kMagic);
+            b[i + j] = __float_as_uint(s);
+            d[j] = __fmaf_rn(a[i + j], r, kMagic - s);
+        }
+        far = max_abs(far, d[0], d[1]);
+    }
+    return low_bytes(b);
+}
+
+// Writes those of eight integers that lie next to a half, on the side that the
+// sign of 254 |a| - (2 floor|t| + 1) m gives (both products exact in double).
+__device__ __noinline__ void decide8(float a0, float a1, float a2, float a3, float a4, float a5,
+                                     float a6, float a7, float m, float r, int8_t* q) {
+    const float a[kVec] = {a0, a1, a2, a3, a4, a5, a6, a7};
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const float s = __fmaf_rn(a[i], r, kMagic);
+        if (fabsf(__fmaf_rn(a[i], r, kMagic - s)) <= kNear) continue;
+        const float f = floorf(fabsf(__fmul_rn(a[i], r)));
+        const double c = 254.0 * static_cast<double>(fabsf(a[i])) -
+                         static_cast<double>(2.0f * f + 1.0f) * static_cast<double>(m);
+        const int k = static_cast<int>(f);
+        const int n = c > 0.0 ? k + 1 : c < 0.0 ? k : k + (k & 1);
+        q[i] = static_cast<int8_t>(a[i] < 0.0f ? -n : n);
+    }
+}
+
+// Rows whose maximum is not in [kLow, kHigh] are scaled by 2^100 first
+// (exactly where it matters), so that 127 / m and 127 a stay finite; rows of
+// zeros, and those with a value that is not finite, give zeros.
+constexpr float kLow = 1e-30f, kHigh = 1e36f;
+__device__ __noinline__ void rare8(float a0, float a1, float a2, float a3, float a4, float a5,
+                                   float a6, float a7, uint32_t mbits, int8_t* q) {
+    if (mbits == 0u || mbits >= 0x7f800000u) {
+        *reinterpret_cast<uint2*>(q) = make_uint2(0, 0);
+        return;
+    }
+    const float up = __uint_as_float(mbits) < kLow ? 0x1p100f : 0x1p-100f;
+    const float a[kVec] = {a0 * up, a1 * up, a2 * up, a3 * up, a4 * up, a5 * up, a6 * up, a7 * up};
+    const float m = __uint_as_float(mbits) * up, r = __fdiv_rn(127.0f, m);
+    float far = 0.0f;
+    *reinterpret_cast<uint2*>(q) = quantize8(a, r, far);
+    decide8(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], m, r, q);
+}
 
 __device__ __forceinline__ double warp_sum_f64(double x) {
 #pragma unroll
@@ -117,52 +184,56 @@ __device__ __forceinline__ double warp_sum_f64(double x) {
 // NG groups of 8 in registers between the two halves of the pass; NG = 0 (rows
 // too long for that) reads them again, from the residual it has just written
 // where there is one.
+constexpr int max_threads(int ng) { return ng == 4 || ng == 8 ? 512 : 1024; }
+
 template <typename XT, typename RT, bool kNorm, int NG>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(max_threads(NG))
 quantize_rows_kernel(const XT* __restrict__ x, const RT* residual, const float* __restrict__ weight,
                      float eps, RT* residual_out, int8_t* __restrict__ q,
                      float* __restrict__ scale, int M, int64_t D) {
     __shared__ double s_sum[32];
     __shared__ uint32_t s_max[32];
     tc::grid_dep_launch();
-    tc::grid_dep_wait();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool live = row < M;
     const int64_t base = row * D;
     const int T = blockDim.x;
     const int n_groups = static_cast<int>(D / kVec);
+    tc::grid_dep_wait();
 
     double sum = 0.0;
-    uint32_t top = 0;
-    // h of a group from its inputs; the statistics' share of it, leaving a
-    auto load = [&](int g, float (&v)[kVec], float (&r)[kVec]) {
-        const int64_t at = base + static_cast<int64_t>(g) * kVec;
-        load8(x + at, v);
-        if (kNorm && residual) load8(residual + at, r);
-    };
-    auto first = [&](int g, float (&a)[kVec], const float (&r)[kVec]) {
+    float top = 0.0f;
+    // a of a group from its inputs, with its share of the statistics; the new
+    // residual is written
+    auto first = [&](int g, const Raw<XT>& xr, const Raw<RT>& rr, float (&a)[kVec]) {
         const int64_t at = static_cast<int64_t>(g) * kVec;
+        xr.unpack(a);
         if constexpr (kNorm) {
             if (residual) {
+                float r[kVec];
+                rr.unpack(r);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) a[i] = __fadd_rn(a[i], r[i]);
             }
             round_to(static_cast<RT*>(nullptr), a);
             if (residual_out) store8(residual_out + base + at, a);
+            Raw<float> wr;
+            wr.load(weight + at);
             float w[kVec];
-            load8(weight + at, w);
+            wr.unpack(w);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
                 sum = fma(static_cast<double>(a[i]), static_cast<double>(a[i]), sum);
                 a[i] = __fmul_rn(a[i], w[i]);
             }
         }
-        // as bits, so that a NaN is above everything and stays
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) top = max(top, __float_as_uint(fabsf(a[i])));
+        for (int i = 0; i < kVec; i += 2) top = max_abs(top, a[i], a[i + 1]);
     };
-    float keep[NG > 0 ? NG : 1][kVec];
-    float res[NG > 0 ? NG : 1][kVec];
+    constexpr int kKeep = NG > 0 ? NG : 1;
+    Raw<XT> xr[kKeep];
+    Raw<RT> rr[kKeep];
+    float keep[kKeep][kVec];
     if (live) {
         if constexpr (NG > 0) {
             // every load of the thread before its first store: the residual
@@ -170,83 +241,145 @@ quantize_rows_kernel(const XT* __restrict__ x, const RT* residual, const float* 
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 const int g = threadIdx.x + i * T;
-                if (g < n_groups) load(g, keep[i], res[i]);
+                if (g < n_groups) {
+                    xr[i].load(x + base + static_cast<int64_t>(g) * kVec);
+                    if (kNorm && residual) rr[i].load(residual + base + static_cast<int64_t>(g) * kVec);
+                }
             }
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 const int g = threadIdx.x + i * T;
-                if (g < n_groups) first(g, keep[i], res[i]);
+                if (g < n_groups) first(g, xr[i], rr[i], keep[i]);
             }
         } else {
             for (int g = threadIdx.x; g < n_groups; g += T) {
-                load(g, keep[0], res[0]);
-                first(g, keep[0], res[0]);
+                xr[0].load(x + base + static_cast<int64_t>(g) * kVec);
+                if (kNorm && residual) rr[0].load(residual + base + static_cast<int64_t>(g) * kVec);
+                first(g, xr[0], rr[0], keep[0]);
             }
         }
     }
 
-    // the row's maximum for every thread, its sum for its first warp
-    top = __reduce_max_sync(kFull, top);
-    if constexpr (kNorm) sum = warp_sum_f64(sum);
+    // the row's maximum for every thread, its sum for its first warp; compared
+    // as bits, where infinities and NaN are above everything
+    uint32_t mbits = __float_as_uint(top);
+    if (T < 32) {                                   // several rows a warp, T a power of two
+        for (int off = T >> 1; off > 0; off >>= 1) {
+            mbits = max(mbits, __shfl_xor_sync(kFull, mbits, off));
+            if constexpr (kNorm) sum += __shfl_xor_sync(kFull, sum, off);
+        }
+    } else {
+        mbits = __reduce_max_sync(kFull, mbits);
+        if constexpr (kNorm) sum = warp_sum_f64(sum);
+    }
     const int warps = T >> 5;                       // warps of a row
     if (warps > 1) {
         const int w0 = threadIdx.y * warps;
         const int lane = threadIdx.x & 31;
         if (lane == 0) {
-            s_max[w0 + (threadIdx.x >> 5)] = top;
+            s_max[w0 + (threadIdx.x >> 5)] = mbits;
             if constexpr (kNorm) s_sum[w0 + (threadIdx.x >> 5)] = sum;
         }
         __syncthreads();
-        top = __reduce_max_sync(kFull, lane < warps ? s_max[w0 + lane] : 0u);
+        mbits = __reduce_max_sync(kFull, lane < warps ? s_max[w0 + lane] : 0u);
         if constexpr (kNorm) {
             if (threadIdx.x < 32) sum = warp_sum_f64(lane < warps ? s_sum[w0 + lane] : 0.0);
         }
     }
     if (!live) return;
-    const RowQuant rq(top);
+    const float m = __uint_as_float(mbits);
+    const bool plain = m >= kLow && m <= kHigh;                 // of the whole row
+    constexpr bool kShort = sizeof(XT) == 2 && !kNorm;           // a is bf16
+    const float r = __fdiv_rn(kShort ? 1.0f : 127.0f, m);
     int8_t* qrow = q + base;
+    auto group = [&](int g) { return qrow + static_cast<int64_t>(g) * kVec; };
+    auto exact = [&](int g, const float (&a)[kVec]) {
+        decide8(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], m, r, group(g));
+    };
+    auto rare = [&](int g, const float (&a)[kVec]) {
+        rare8(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], mbits, group(g));
+    };
     if constexpr (NG > 0) {
+        // one test for all of the thread's integers: next to a half lies one
+        // in 32768
+        float far = 0.0f;
+        if (plain) {
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-            const int g = threadIdx.x + i * T;
-            if (g < n_groups)
-                *reinterpret_cast<uint2*>(qrow + static_cast<int64_t>(g) * kVec) = rq.pack8(keep[i]);
+            for (int i = 0; i < NG; ++i) {
+                const int g = threadIdx.x + i * T;
+                if (g < n_groups)
+                    *reinterpret_cast<uint2*>(group(g)) =
+                        kShort ? quantize8_bf16(keep[i], m, r) : quantize8(keep[i], r, far);
+            }
+        }
+        if (!plain || far > kNear) {
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                const int g = threadIdx.x + i * T;
+                if (g < n_groups) {
+                    if (plain) exact(g, keep[i]);
+                    else rare(g, keep[i]);
+                }
+            }
         }
     } else {
         for (int g = threadIdx.x; g < n_groups; g += T) {
             const int64_t at = static_cast<int64_t>(g) * kVec;
             float a[kVec];
             if (kNorm && residual_out) {
-                load8(residual_out + base + at, a);       // this thread wrote it above
+                Raw<RT> h;
+                h.load(residual_out + base + at);         // this thread wrote it above
+                h.unpack(a);
             } else {
-                float r[kVec];
-                load(g, a, r);
+                xr[0].load(x + base + at);
+                xr[0].unpack(a);
                 if (kNorm && residual) {
+                    float f[kVec];
+                    rr[0].load(residual + base + at);
+                    rr[0].unpack(f);
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) a[i] = __fadd_rn(a[i], r[i]);
+                    for (int i = 0; i < kVec; ++i) a[i] = __fadd_rn(a[i], f[i]);
                 }
                 if constexpr (kNorm) round_to(static_cast<RT*>(nullptr), a);
             }
             if constexpr (kNorm) {
+                Raw<float> wr;
                 float w[kVec];
-                load8(weight + at, w);
+                wr.load(weight + at);
+                wr.unpack(w);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) a[i] = __fmul_rn(a[i], w[i]);
             }
-            *reinterpret_cast<uint2*>(qrow + at) = rq.pack8(a);
+            if (plain) {
+                float far = 0.0f;
+                *reinterpret_cast<uint2*>(group(g)) =
+                    kShort ? quantize8_bf16(a, m, r) : quantize8(a, r, far);
+                if (far > kNear) exact(g, a);
+            } else {
+                rare(g, a);
+            }
         }
     }
     if (threadIdx.x == 0) {
-        double s = static_cast<double>(__uint_as_float(top)) / 127.0;
+        double s = static_cast<double>(m) / 127.0;
         if constexpr (kNorm)
             s /= sqrt(sum / static_cast<double>(D) + static_cast<double>(eps));
-        scale[row] = top == 0u ? 0.0f : top >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                                           : static_cast<float>(s);
+        scale[row] = mbits == 0u ? 0.0f : mbits >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                                                               : static_cast<float>(s);
     }
 }
 
 template <typename XT, typename RT, bool kNorm, int NG>
-cudaError_t launch_rows(const RowsI8Args& a, int threads, int rows, cudaStream_t stream) {
+cudaError_t launch_rows(const RowsI8Args& a, cudaStream_t stream) {
+    const int64_t groups = a.D / kVec;
+    int threads = max_threads(0);
+    if constexpr (NG > 0) {
+        const int64_t need = (groups + NG - 1) / NG;
+        threads = 2;
+        while (threads < 32 && threads < need) threads *= 2;
+        if (need > 32) threads = static_cast<int>((need + 31) / 32 * 32);
+    }
+    const int rows = threads >= 128 ? 1 : 128 / threads;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.M + rows - 1) / rows));
     cfg.blockDim = dim3(static_cast<unsigned>(threads), static_cast<unsigned>(rows));
@@ -262,17 +395,35 @@ cudaError_t launch_rows(const RowsI8Args& a, int threads, int rows, cudaStream_t
                               static_cast<int>(a.M), a.D);
 }
 
+// Groups a thread. Few rows: one, so that a row is spread over as many threads
+// as there are (64 x 2048 in 2.3 us against 4.3 with four). Many rows (a
+// million threads with one group each, some three waves): as many as put 64 to
+// 128 bytes a thread on their way, since what a row costs beside its elements
+// is shared by fewer threads (4096 x 8192 bf16 quantised: 22.7 with four,
+// 31.7 with one; bf16 norm 40.9 against 50.8; but fp32 norm of 4096 x 4096
+// 39.4 with four, 35.9 with one, and of 4096 x 8192 75.4 with two, 88.7 with
+// one).
+template <typename XT, typename RT, bool kNorm>
+int groups_a_thread(int64_t M, int64_t groups) {
+    const int least = groups <= 1024 ? 1 : groups <= 2048 ? 2 : groups <= 4096 ? 8 : 0;
+    if (least != 1 && least != 2) return least;
+    if (M * groups < (1 << 20)) return least;
+    if (kNorm && sizeof(XT) + sizeof(RT) > 4) return groups > 512 ? 2 : 1;
+    if (kNorm) return groups >= 256 ? 4 : 1;
+    return groups >= 128 ? 4 : groups >= 64 ? 2 : 1;
+}
+
 template <typename XT, typename RT, bool kNorm>
 cudaError_t launch_typed(const RowsI8Args& a, cudaStream_t stream) {
     const int64_t groups = a.D / kVec;
-    int64_t ng = (groups + kMaxThreads - 1) / kMaxThreads;
-    const int threads = static_cast<int>(std::min<int64_t>(
-        kMaxThreads, ((groups + (ng <= 1 ? 1 : ng) - 1) / (ng <= 1 ? 1 : ng) + 31) / 32 * 32));
-    const int rows = threads >= 256 ? 1 : 256 / threads;
-    if (ng <= 1) return launch_rows<XT, RT, kNorm, 1>(a, threads, rows, stream);
-    if (ng <= 2) return launch_rows<XT, RT, kNorm, 2>(a, threads, rows, stream);
-    if (ng <= kMaxGroups) return launch_rows<XT, RT, kNorm, kMaxGroups>(a, threads, rows, stream);
-    return launch_rows<XT, RT, kNorm, 0>(a, kMaxThreads, 1, stream);
+    const int ng = groups_a_thread<XT, RT, kNorm>(a.M, groups);
+    switch (ng) {
+        case 1: return launch_rows<XT, RT, kNorm, 1>(a, stream);
+        case 2: return launch_rows<XT, RT, kNorm, 2>(a, stream);
+        case 4: return launch_rows<XT, RT, kNorm, 4>(a, stream);
+        case 8: return launch_rows<XT, RT, kNorm, 8>(a, stream);
+        default: return launch_rows<XT, RT, kNorm, 0>(a, stream);
+    }
 }
 
 }  // namespace
