@@ -584,31 +584,70 @@ def _check(t, name, dtypes, shape, device):
         _refuse(t, name, dtypes, shape, device)
 
 
-def _rows_args(x, q, scale):
+def _lead(t):
+    """The leading sizes of t [..., D] and their product."""
+    shape = t.shape
+    if len(shape) == 2:
+        return (shape[0],), shape[0]
+    return shape[:-1], shape[:-1].numel()
+
+
+def _launch(fn, name, dev, args, stream):
+    """Call `fn` with device number `dev` current on `stream`."""
+    st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status:
+        _raise_on(name, status)
+
+
+# The three calls below are short on the device (2 to 10 us at decode sizes),
+# so what is right is recognised in one expression and everything else left to
+# the checks that name what is wrong.
+
+def _rows_i8_refuse(x, q, scale, weight=None, residual=None, residual_out=None):
+    """Raise for what quantize_i8 or add_rms_norm_i8 found wrong."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be a tensor [..., D]")
-    shape, dev = x.shape, x.get_device()
+    dev, shape = x.get_device(), x.shape
     _check(x, "x", _FLOATS, shape, dev)
-    lead = shape[:-1]
-    if q is None:
-        q = torch.empty(shape, dtype=torch.int8, device=x.device)
-    else:
-        _check(q, "q", _I8_ONLY, shape, dev)
-    if scale is None:
-        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
-    else:
-        _check(scale, "scale", _F32_ONLY, lead, dev)
-    return x.device, dev, lead.numel(), shape[-1], q, scale
+    for t, name, dtypes, want in ((q, "q", _I8_ONLY, shape), (scale, "scale", _F32_ONLY, shape[:-1]),
+                                  (weight, "weight", _F32_ONLY, shape[-1:]),
+                                  (residual, "residual", _FLOATS, shape),
+                                  (residual_out, "residual_out", _FLOATS, shape)):
+        if t is not None:
+            _check(t, name, dtypes, want, dev)
+    if residual is not None and residual_out is not None:
+        _check(residual_out, "residual_out", (residual.dtype,), shape, dev)
+    raise TypeError("weight must be a torch.Tensor")
 
 
 def quantize_i8(x, q=None, scale=None, *, stream=None):
     """Rows of x [..., D] (fp32 or bf16, D a multiple of 16) in 8-bit integers
     with one scale a row: activations by token, weights [N, K] by output
     channel. Returns (q [..., D] int8, scale [...] fp32), q * scale ~ x."""
-    device, _, M, D, q, scale = _rows_args(x, q, scale)
-    st = _call(device, load_library().gdn_quantize_i8, x.data_ptr(), _DTYPES[x.dtype],
-               q.data_ptr(), scale.data_ptr(), M, D, _stream(device, stream))
-    _raise_on("gdn_quantize_i8", st)
+    try:
+        shape, dev, dtype = x.shape, x.get_device(), x.dtype
+        D = shape[-1]
+        lead, M = _lead(x)
+        good = (dev >= 0 and dtype in _DTYPES and x.is_contiguous()
+                and (q is None or (q.dtype is torch.int8 and q.shape == shape
+                                   and q.get_device() == dev and q.is_contiguous()))
+                and (scale is None or (scale.dtype is torch.float32 and scale.shape == lead
+                                       and scale.get_device() == dev and scale.is_contiguous())))
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _rows_i8_refuse(x, q, scale)
+    if q is None:
+        q = torch.empty(shape, dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+    _launch(load_library().gdn_quantize_i8, "gdn_quantize_i8", dev,
+            (x.data_ptr(), _DTYPES[dtype], q.data_ptr(), scale.data_ptr(), M, D), stream)
     return q, scale
 
 
@@ -619,24 +658,56 @@ def add_rms_norm_i8(x, weight, residual=None, residual_out=None, q=None, scale=N
     or bf16, residual and residual_out [..., D] fp32 or bf16, weight [D] fp32.
     residual_out receives h (it may be `residual`; a new tensor when only
     `residual` is given). Returns (q, scale, residual_out or None)."""
-    device, dev, M, D, q, scale = _rows_args(x, q, scale)
-    _check(weight, "weight", _F32_ONLY, (D,), dev)
-    rtype = 0
-    if residual is not None:
-        _check(residual, "residual", _FLOATS, x.shape, dev)
-        rtype = _DTYPES[residual.dtype]
-        if residual_out is None:
-            residual_out = torch.empty_like(residual)
-    if residual_out is not None:
-        _check(residual_out, "residual_out",
-               _FLOATS if residual is None else (residual.dtype,), x.shape, dev)
-        rtype = _DTYPES[residual_out.dtype]
-    st = _call(device, load_library().gdn_add_rms_norm_i8, x.data_ptr(), _DTYPES[x.dtype],
-               None if residual is None else residual.data_ptr(), weight.data_ptr(), eps,
-               None if residual_out is None else residual_out.data_ptr(), rtype, q.data_ptr(),
-               scale.data_ptr(), M, D, _stream(device, stream))
-    _raise_on("gdn_add_rms_norm_i8", st)
+    try:
+        shape, dev, dtype = x.shape, x.get_device(), x.dtype
+        D = shape[-1]
+        lead, M = _lead(x)
+        rdtype = (residual.dtype if residual is not None else
+                  residual_out.dtype if residual_out is not None else torch.float32)
+        good = (dev >= 0 and dtype in _DTYPES and rdtype in _DTYPES and x.is_contiguous()
+                and weight.dtype is torch.float32 and weight.shape == (D,)
+                and weight.get_device() == dev and weight.is_contiguous()
+                and (residual is None or (residual.shape == shape and residual.get_device() == dev
+                                          and residual.is_contiguous()))
+                and (residual_out is None or (residual_out.dtype is rdtype
+                                              and residual_out.shape == shape
+                                              and residual_out.get_device() == dev
+                                              and residual_out.is_contiguous()))
+                and (q is None or (q.dtype is torch.int8 and q.shape == shape
+                                   and q.get_device() == dev and q.is_contiguous()))
+                and (scale is None or (scale.dtype is torch.float32 and scale.shape == lead
+                                       and scale.get_device() == dev and scale.is_contiguous())))
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _rows_i8_refuse(x, q, scale, weight, residual, residual_out)
+    if q is None:
+        q = torch.empty(shape, dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    _launch(load_library().gdn_add_rms_norm_i8, "gdn_add_rms_norm_i8", dev,
+            (x.data_ptr(), _DTYPES[dtype], None if residual is None else residual.data_ptr(),
+             weight.data_ptr(), eps, None if residual_out is None else residual_out.data_ptr(),
+             _DTYPES[rdtype], q.data_ptr(), scale.data_ptr(), M, D), stream)
     return q, scale, residual_out
+
+
+def _linear_i8_refuse(x, x_scale, w, w_scale, y):
+    """Raise for what linear_i8 found wrong (y may be None)."""
+    if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor):
+        raise TypeError("x and w must be tensors")
+    if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
+        raise ValueError("x must be [..., K] and w [N, K]")
+    dev, lead = x.get_device(), x.shape[:-1]
+    _check(x, "x", _I8_ONLY, x.shape, dev)
+    _check(x_scale, "x_scale", _F32_ONLY, lead, dev)
+    _check(w, "w", _I8_ONLY, w.shape, dev)
+    _check(w_scale, "w_scale", _F32_ONLY, w.shape[:1], dev)
+    if y is not None:
+        _check(y, "y", _FLOATS, (*lead, w.shape[0]), dev)
+    raise ValueError("linear_i8: arguments do not belong together")
 
 
 def linear_i8(x, x_scale, w, w_scale, y=None, *, out_dtype=torch.float32, status=None,
@@ -645,33 +716,34 @@ def linear_i8(x, x_scale, w, w_scale, y=None, *, out_dtype=torch.float32, status
     [...], w [N, K] int8 with w_scale [N], exact integer sums (K a multiple of
     16, at most 131056). y [..., N] has `out_dtype` (fp32 or bf16), or its own
     type when given. `status` as for linear_bf16."""
-    if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor):
-        raise TypeError("x and w must be tensors")
-    xshape, wshape, dev = x.shape, w.shape, x.get_device()
-    if len(wshape) != 2 or not xshape or xshape[-1] != wshape[1]:
-        raise ValueError("x must be [..., K] and w [N, K]")
-    N, K = wshape
-    lead = xshape[:-1]
-    _check(x, "x", _I8_ONLY, xshape, dev)
-    _check(x_scale, "x_scale", _F32_ONLY, lead, dev)
-    _check(w, "w", _I8_ONLY, wshape, dev)
-    _check(w_scale, "w_scale", _F32_ONLY, (N,), dev)
-    device = x.device
+    try:
+        N, K = w.shape
+        lead, M = _lead(x)
+        dev = x.get_device()
+        good = (dev >= 0 and x.dtype is torch.int8 and w.dtype is torch.int8
+                and x_scale.dtype is torch.float32 and w_scale.dtype is torch.float32
+                and x.shape[-1] == K and x_scale.shape == lead and w_scale.shape == (N,)
+                and w.get_device() == dev and x_scale.get_device() == dev
+                and w_scale.get_device() == dev and x.is_contiguous() and w.is_contiguous()
+                and x_scale.is_contiguous() and w_scale.is_contiguous()
+                and (y is None or (y.dtype in _DTYPES and y.shape == (*lead, N)
+                                   and y.get_device() == dev and y.is_contiguous())))
+    except (AttributeError, IndexError, ValueError):
+        good = False
+    if not good:
+        _linear_i8_refuse(x, x_scale, w, w_scale, y)
     if y is None:
         if out_dtype not in _DTYPES:
             raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
-        y = torch.empty((*lead, N), dtype=out_dtype, device=device)
-    else:
-        _check(y, "y", _FLOATS, (*lead, N), dev)
+        y = torch.empty((*lead, N), dtype=out_dtype, device=x.device)
     sp = None
     if status is not None:
-        if status.dtype is not torch.int32 or status.device != device or status.numel() != 1:
+        if status.dtype is not torch.int32 or status.device != x.device or status.numel() != 1:
             raise TypeError("status must be a one-element int32 tensor on the same device")
         sp = status.data_ptr()
-    st = _call(device, load_library().gdn_linear_i8, x.data_ptr(), x_scale.data_ptr(),
-               w.data_ptr(), w_scale.data_ptr(), y.data_ptr(), _DTYPES[y.dtype], lead.numel(), N,
-               K, sp, _stream(device, stream))
-    _raise_on("gdn_linear_i8", st)
+    _launch(load_library().gdn_linear_i8, "gdn_linear_i8", dev,
+            (x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), y.data_ptr(),
+             _DTYPES[y.dtype], M, N, K, sp), stream)
     return y
 
 
