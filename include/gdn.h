@@ -373,6 +373,33 @@ gdn_status gdn_forward_batch(const void *hidden, const void *w_qkv, const void *
                              int64_t dv, int64_t K, uint32_t *status, void *stream);
 
 /*
+ * gdn_forward_batch_i8 -- gdn_forward_batch with 8-bit projections: its input
+ * is what gdn_add_rms_norm_i8 (or gdn_quantize_i8) leaves, its weights are
+ * gdn_quantize_i8's, and its projections are gdn_linear_i8's. Stage 6's row
+ * y (all heads of a position) is quantised by position, as gdn_quantize_i8
+ * does, before the output projection:
+ *   mixed, z, (b | a) = gdn_linear_i8 of hidden
+ *   stages 1-6 of gdn_layer_decode, as in gdn_forward_batch
+ *   y in 8-bit integers, out = gdn_linear_i8 of y
+ *
+ *   hidden [B][T][D] int8, hidden_scale [B][T]    D a multiple of 16
+ *   w_qkv [C][D], w_z [Hv*dv][D], w_ba [2*Hv][D], w_out [D][Hv*dv] int8
+ *   s_qkv [C], s_z [Hv*dv], s_ba [2*Hv], s_out [D]
+ *   out    [B][T][D] fp32 or bf16 (out_type)
+ * D and Hv*dv at most 131056 (gdn_linear_i8's K). Everything else (the
+ * workspace and its size function, limits, status, aliasing) as
+ * gdn_forward_batch.
+ */
+gdn_status gdn_forward_batch_i8(
+    const int8_t *hidden, const float *hidden_scale, const int8_t *w_qkv, const float *s_qkv,
+    const int8_t *w_z, const float *s_z, const int8_t *w_ba, const float *s_ba,
+    const int8_t *w_out, const float *s_out, float *conv_ring, const float *conv_w,
+    const float *A_log, const float *dt_bias, const float *norm_w, float l2_eps, float norm_eps,
+    float *state, void *out, int out_type, void *workspace, size_t workspace_bytes, int64_t B,
+    int64_t T, int64_t D, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t K,
+    uint32_t *status, void *stream);
+
+/*
  * gdn_forward_batch_noalloc -- gdn_forward_batch without a caller-provided
  * workspace, for callers that cannot allocate device memory (a plugin whose
  * host program owns every device allocation and offers no hook, code held to

@@ -10,7 +10,7 @@ _BINDING = ("GdnError", "step", "prefill", "pair", "layer_decode", "layer_pair",
             "forward_batch", "forward_batch_workspace_size", "forward_batch_noalloc",
             "short_conv_forward", "short_conv_forward_batch", "short_conv_pair",
             "short_conv_workspace_size", "kda_step", "kda_prefill", "quantize_i8",
-            "add_rms_norm_i8", "linear_i8", "library_path",
+            "add_rms_norm_i8", "linear_i8", "forward_batch_i8", "library_path",
             "status_string")
 
 

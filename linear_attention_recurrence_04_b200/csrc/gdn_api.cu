@@ -581,6 +581,69 @@ size_t gdn_forward_batch_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_
     return forward_batch_layout(B, T, static_cast<int>(Hk), static_cast<int>(Hv)).total;
 }
 
+gdn_status gdn_forward_batch_i8(
+    const int8_t* hidden, const float* hidden_scale, const int8_t* w_qkv, const float* s_qkv,
+    const int8_t* w_z, const float* s_z, const int8_t* w_ba, const float* s_ba,
+    const int8_t* w_out, const float* s_out, float* conv_ring, const float* conv_w,
+    const float* A_log, const float* dt_bias, const float* norm_w, float l2_eps, float norm_eps,
+    float* state, void* out, int out_type, void* workspace, size_t workspace_bytes, int64_t B,
+    int64_t T, int64_t D, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t K,
+    uint32_t* status, void* stream) {
+    NvtxRange nvtx_range("gdn_forward_batch_i8");
+    const char* fn = "gdn_forward_batch_i8";
+    if (B < 0 || T < 0 || D < 0) return fail(GDN_ERR_SHAPE, "%s: negative B, T or D", fn);
+    gdn_status st = check_geometry(Hk, Hv, dk, dv);
+    if (st != GDN_OK) return st;
+    if (K != kConvK) return fail(GDN_ERR_UNSUPPORTED, "%s: K=%lld: only a conv kernel of 4 is implemented",
+                                 fn, (long long)K);
+    if (!known_type(out_type)) return fail(GDN_ERR_UNSUPPORTED, "%s: unknown type %d", fn, out_type);
+    if (D == 0 || D % 16 != 0 || D > kLinearI8MaxK || Hv * dv > kLinearI8MaxK)
+        return fail(GDN_ERR_UNSUPPORTED, "%s: D=%lld must be a positive multiple of 16, D and Hv*dv at most %lld",
+                    fn, (long long)D, (long long)kLinearI8MaxK);
+    if (B > 65535 || T > (int64_t)65535 * 32 || B * T > (int64_t)65535 * 128)
+        return fail(GDN_ERR_OVERFLOW, "%s: B=%lld, T=%lld or B*T too large", fn, (long long)B,
+                    (long long)T);
+    const int64_t BT = B * T;
+    const int64_t C = 2 * Hk * dk + Hv * dv;
+    const int64_t HD = Hv * dv;
+    if (BT == 0) { g_last_error[0] = '\0'; return GDN_OK; }
+    const size_t need = forward_batch_layout(B, T, static_cast<int>(Hk), static_cast<int>(Hv)).total;
+    const Span ins[] = {{state, B * Hv * dv * dk * 4, "state"},
+                        {conv_ring, B * (K - 1) * C * 4, "conv_ring"},
+                        {workspace, static_cast<int64_t>(need), "workspace"},
+                        {status, status ? 4 : 0, "status"},
+                        {hidden, BT * D, "hidden"}, {hidden_scale, BT * 4, "hidden_scale"},
+                        {w_qkv, C * D, "w_qkv"}, {s_qkv, C * 4, "s_qkv"},
+                        {w_z, HD * D, "w_z"}, {s_z, HD * 4, "s_z"},
+                        {w_ba, 2 * Hv * D, "w_ba"}, {s_ba, 2 * Hv * 4, "s_ba"},
+                        {w_out, D * HD, "w_out"}, {s_out, D * 4, "s_out"},
+                        {conv_w, C * K * 4, "conv_w"}, {A_log, Hv * 4, "A_log"},
+                        {dt_bias, Hv * 4, "dt_bias"}, {norm_w, dv * 4, "norm_w"}};
+    constexpr int kIns = sizeof(ins) / sizeof(ins[0]);
+    for (const Span& i : ins)
+        if (!i.p && &i != &ins[3]) return fail(GDN_ERR_NULL, "%s: %s is NULL", fn, i.name);
+    if (!out) return fail(GDN_ERR_NULL, "%s: out is NULL", fn);
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_SHAPE, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+    for (const void* p : {(const void*)hidden, (const void*)w_qkv, (const void*)w_z,
+                          (const void*)w_ba, (const void*)w_out, (const void*)conv_ring,
+                          (const void*)conv_w, (const void*)state, (const void*)out})
+        if (!aligned(p, 16)) return fail(GDN_ERR_ALIGN, "%s: alignment rule violated", fn);
+    for (const void* p : {(const void*)hidden_scale, (const void*)s_qkv, (const void*)s_z,
+                          (const void*)s_ba, (const void*)s_out, (const void*)A_log,
+                          (const void*)dt_bias, (const void*)norm_w, (const void*)status})
+        if (!aligned(p, 4)) return fail(GDN_ERR_ALIGN, "%s: alignment rule violated", fn);
+    if (!aligned(workspace, 256))
+        return fail(GDN_ERR_ALIGN, "%s: workspace needs 256-byte alignment", fn);
+    st = check_spans(ins, kIns, 4, Span{out, BT * D * (out_type == GDN_BF16 ? 2 : 4), "out"});
+    if (st != GDN_OK) return st;
+    ForwardBatchArgs a{hidden, w_qkv, w_z, w_ba, w_out, conv_ring, conv_w, A_log, dt_bias, norm_w,
+                       l2_eps, norm_eps, state, out, workspace, B, T, D, static_cast<int>(Hk),
+                       static_cast<int>(Hv), status};
+    ForwardBatchI8 e{hidden_scale, s_qkv, s_z, s_ba, s_out, out_type == GDN_BF16};
+    return launched(launch_forward_batch_i8(a, e, static_cast<cudaStream_t>(stream)), fn);
+}
+
 gdn_status gdn_forward_batch(const void* hidden, const void* w_qkv, const void* w_z,
                              const void* w_ba, const void* w_out, float* conv_ring,
                              const float* conv_w, const float* A_log, const float* dt_bias,

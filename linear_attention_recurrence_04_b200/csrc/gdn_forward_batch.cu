@@ -21,6 +21,10 @@
 //   5. tail: per (position, value head) gated RMSNorm in double, rounded to
 //      bf16 (the output projection's input type);
 //   6. out = y . W_out^T (tcgen05 GEMM).
+//
+// With 8-bit projections (launch_forward_batch_i8) the products of 1 and 6 are
+// gdn_linear_i8's and the tail of 5 leaves y in 8-bit integers with a scale a
+// position; 2 to 4 are the same kernels.
 #include <cuda_bf16.h>
 
 #include "gdn_common.cuh"
@@ -209,31 +213,21 @@ ForwardBatchLayout forward_batch_layout(int64_t B, int64_t T, int Hk, int Hv) {
     return L;
 }
 
-cudaError_t launch_forward_batch(const ForwardBatchArgs& a, cudaStream_t stream) {
+namespace {
+
+// Stages 2 to 4, from the projections in the workspace to o.
+cudaError_t launch_middle(const ForwardBatchArgs& a, const ForwardBatchLayout& L,
+                          cudaStream_t stream) {
     const int64_t BT = a.B * a.T;
-    if (BT == 0) return cudaSuccess;
     const int64_t C = static_cast<int64_t>(2 * a.Hk) * kDk + static_cast<int64_t>(a.Hv) * kDv;
-    const int64_t HD = static_cast<int64_t>(a.Hv) * kDv;
-    const ForwardBatchLayout L = forward_batch_layout(a.B, a.T, a.Hk, a.Hv);
     char* ws = static_cast<char*>(a.workspace);
     float* act = reinterpret_cast<float*>(ws + L.act);
-    float* z = reinterpret_cast<float*>(ws + L.z);
     float* ba = reinterpret_cast<float*>(ws + L.ba);
     float* beta = reinterpret_cast<float*>(ws + L.beta);
     float* gate = reinterpret_cast<float*>(ws + L.gate);
     float* o = reinterpret_cast<float*>(ws + L.o);
-    __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(ws + L.y);
     float* halo = reinterpret_cast<float*>(ws + L.halo);
-
-    // 1. input projections
     cudaError_t err;
-    if ((err = launch_linear_bf16(LinearArgs{a.hidden, a.w_qkv, act, BT, C, a.D, a.status}, stream)))
-        return err;
-    if ((err = launch_linear_bf16(LinearArgs{a.hidden, a.w_z, z, BT, HD, a.D, a.status}, stream)))
-        return err;
-    if ((err = launch_linear_bf16(LinearArgs{a.hidden, a.w_ba, ba, BT, 2 * a.Hv, a.D, a.status},
-                                  stream)))
-        return err;
     // 2. conv over positions with the ring, SiLU (halo pass, then in place)
     {
         const int n_tiles = static_cast<int>((a.T + kConvTile - 1) / kConvTile);
@@ -259,6 +253,35 @@ cudaError_t launch_forward_batch(const ForwardBatchArgs& a, cudaStream_t stream)
         p.status = a.status;
         if ((err = launch_prefill(p, stream))) return err;
     }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_forward_batch(const ForwardBatchArgs& a, cudaStream_t stream) {
+    const int64_t BT = a.B * a.T;
+    if (BT == 0) return cudaSuccess;
+    const int64_t C = static_cast<int64_t>(2 * a.Hk) * kDk + static_cast<int64_t>(a.Hv) * kDv;
+    const int64_t HD = static_cast<int64_t>(a.Hv) * kDv;
+    const ForwardBatchLayout L = forward_batch_layout(a.B, a.T, a.Hk, a.Hv);
+    char* ws = static_cast<char*>(a.workspace);
+    float* act = reinterpret_cast<float*>(ws + L.act);
+    float* z = reinterpret_cast<float*>(ws + L.z);
+    float* ba = reinterpret_cast<float*>(ws + L.ba);
+    float* o = reinterpret_cast<float*>(ws + L.o);
+    __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(ws + L.y);
+
+    // 1. input projections
+    cudaError_t err;
+    if ((err = launch_linear_bf16(LinearArgs{a.hidden, a.w_qkv, act, BT, C, a.D, a.status}, stream)))
+        return err;
+    if ((err = launch_linear_bf16(LinearArgs{a.hidden, a.w_z, z, BT, HD, a.D, a.status}, stream)))
+        return err;
+    if ((err = launch_linear_bf16(LinearArgs{a.hidden, a.w_ba, ba, BT, 2 * a.Hv, a.D, a.status},
+                                  stream)))
+        return err;
+    // 2. to 4. conv, q/k norms and gates, the recurrence
+    if ((err = launch_middle(a, L, stream))) return err;
     // 5. gated RMSNorm tail -> bf16
     {
         const int64_t rows = BT * a.Hv;
@@ -267,7 +290,37 @@ cudaError_t launch_forward_batch(const ForwardBatchArgs& a, cudaStream_t stream)
         if ((err = cudaGetLastError())) return err;
     }
     // 6. output projection
-    return launch_linear_bf16(LinearArgs{y, a.w_out, a.out, BT, a.D, HD, a.status}, stream);
+    return launch_linear_bf16(LinearArgs{y, a.w_out, static_cast<float*>(a.out), BT, a.D, HD, a.status}, stream);
+}
+
+cudaError_t launch_forward_batch_i8(const ForwardBatchArgs& a, const ForwardBatchI8& e,
+                                    cudaStream_t stream) {
+    const int64_t BT = a.B * a.T;
+    if (BT == 0) return cudaSuccess;
+    const int64_t C = static_cast<int64_t>(2 * a.Hk) * kDk + static_cast<int64_t>(a.Hv) * kDv;
+    const int64_t HD = static_cast<int64_t>(a.Hv) * kDv;
+    const ForwardBatchLayout L = forward_batch_layout(a.B, a.T, a.Hk, a.Hv);
+    char* ws = static_cast<char*>(a.workspace);
+    float* z = reinterpret_cast<float*>(ws + L.z);
+    const auto project = [&](const void* x, const float* xs, const void* w, const float* s,
+                             void* y, bool y_bf16, int64_t N, int64_t K) {
+        return launch_linear_i8(LinearI8Args{static_cast<const int8_t*>(x), xs,
+                                             static_cast<const int8_t*>(w), s, y, y_bf16, BT, N,
+                                             K, a.status}, stream);
+    };
+    cudaError_t err;
+    if ((err = project(a.hidden, e.hidden_scale, a.w_qkv, e.s_qkv, ws + L.act, false, C, a.D)) ||
+        (err = project(a.hidden, e.hidden_scale, a.w_z, e.s_z, z, false, HD, a.D)) ||
+        (err = project(a.hidden, e.hidden_scale, a.w_ba, e.s_ba, ws + L.ba, false, 2 * a.Hv, a.D)))
+        return err;
+    if ((err = launch_middle(a, L, stream))) return err;
+    // y in 8 bits where the bf16 layer keeps y; its scales where beta was
+    int8_t* y = reinterpret_cast<int8_t*>(ws + L.y);
+    float* y_scale = reinterpret_cast<float*>(ws + L.beta);
+    if ((err = launch_gated_norm_i8(GatedNormI8Args{reinterpret_cast<float*>(ws + L.o), z, a.norm_w,
+                                                    a.norm_eps, y, y_scale, BT, a.Hv}, stream)))
+        return err;
+    return project(y, y_scale, a.w_out, e.s_out, a.out, e.out_bf16, a.D, HD);
 }
 
 }  // namespace gdn

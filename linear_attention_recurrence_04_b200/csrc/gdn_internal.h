@@ -118,7 +118,7 @@ struct ForwardBatchArgs {
     float l2_eps;
     float norm_eps;
     float* state;
-    float* out;            // [B][T][D]
+    void* out;             // [B][T][D] fp32 (bf16 too with 8-bit projections)
     void* workspace;
     int64_t B;
     int64_t T;
@@ -126,6 +126,30 @@ struct ForwardBatchArgs {
     int Hk;
     int Hv;
     uint32_t* status;
+};
+
+// The 8-bit projections' scales (hidden and the weights of ForwardBatchArgs
+// are then signed bytes) and the output's type.
+struct ForwardBatchI8 {
+    const float* hidden_scale;   // [B][T]
+    const float* s_qkv;          // [C]
+    const float* s_z;            // [Hv*dv]
+    const float* s_ba;           // [2*Hv]
+    const float* s_out;          // [D]
+    bool out_bf16;
+};
+
+// The layer's gated RMS norm with its rows (all heads of a position) in 8-bit
+// integers with a scale a row (gdn_quantize_i8.cu).
+struct GatedNormI8Args {
+    const float* o;        // [M][Hv][dv]
+    const float* z;        // [M][Hv][dv]
+    const float* norm_w;   // [dv]
+    float eps;
+    int8_t* q;             // [M][Hv][dv]
+    float* scale;          // [M]
+    int64_t M;
+    int Hv;
 };
 
 // Byte offsets of the forward-batch intermediates inside the workspace.
@@ -186,7 +210,10 @@ cudaError_t launch_linear_bf16(const LinearArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_bf16_split(const LinearArgs& a, cudaStream_t stream);
 cudaError_t launch_rows_i8(const RowsI8Args& a, cudaStream_t stream);
 cudaError_t launch_linear_i8(const LinearI8Args& a, cudaStream_t stream);
+cudaError_t launch_gated_norm_i8(const GatedNormI8Args& a, cudaStream_t stream);
 cudaError_t launch_forward_batch(const ForwardBatchArgs& a, cudaStream_t stream);
+cudaError_t launch_forward_batch_i8(const ForwardBatchArgs& a, const ForwardBatchI8& e,
+                                    cudaStream_t stream);
 cudaError_t launch_short_conv(const ShortConvArgs& a, cudaStream_t stream);
 
 // Value-heads-per-key-head ratios the fused layer kernel is compiled for.

@@ -24,7 +24,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "gdn_common.cuh"
@@ -618,7 +617,7 @@ template <int MT, int R, int W, typename YT>
 __global__ void __launch_bounds__(kVecThreads)
 linear_i8_vec_kernel(const int8_t* __restrict__ x, const float* __restrict__ x_scale,
                      const int8_t* __restrict__ w, const float* __restrict__ w_scale,
-                     YT* __restrict__ y, int M, int N, int K) {
+                     YT* __restrict__ y, int M, int N, int K, int n_blocks) {
     constexpr int kWarps = kVecThreads / 32;
     constexpr int U = 2;                               // pieces of a row in flight
     constexpr int kSpan = 512 * W;                     // bytes that W warps read at once
@@ -626,8 +625,8 @@ linear_i8_vec_kernel(const int8_t* __restrict__ x, const float* __restrict__ x_s
     __shared__ int part[W > 1 ? kWarps : 1][MT * R];
     const int lane = threadIdx.x & 31;
     const int warp = tc::warp_index();
-    const int n0 = (static_cast<int>(blockIdx.x) * (kWarps / W) + warp / W) * R;
-    const int m0 = static_cast<int>(blockIdx.y) * MT;
+    const int n0 = (static_cast<int>(blockIdx.x) % n_blocks * (kWarps / W) + warp / W) * R;
+    const int m0 = static_cast<int>(blockIdx.x) / n_blocks * MT;
     const int at = warp % W * 32 + lane;               // this thread's place in a row
     tc::grid_dep_launch();
     const int8_t* wr[R];
@@ -710,18 +709,11 @@ bool make_tmap_i8(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, in
            CUDA_SUCCESS;
 }
 
-constexpr int kDevs = 16;
-
-// Raises the kernel's shared-memory limit once per device.
-cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<bool> (&done)[kDevs]) {
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < kDevs && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(bytes));
-    if (err == cudaSuccess && dev < kDevs) done[dev].store(true, std::memory_order_release);
-    return err;
+// Raises the kernel's shared-memory limit (at every launch: it belongs to the
+// context, which a program may replace).
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(bytes));
 }
 
 cudaLaunchConfig_t cluster_config(unsigned grid, int threads, int cluster, size_t smem,
@@ -744,10 +736,8 @@ cudaLaunchConfig_t cluster_config(unsigned grid, int threads, int cluster, size_
 
 template <int MC, typename YT>
 cudaError_t launch_split(const LinearI8Args& a, int splits, cudaStream_t stream) {
-    static std::atomic<bool> done[kDevs];
     const auto kernel = linear_i8_split_kernel<MC, YT>;
-    cudaError_t err =
-        allow_smem(reinterpret_cast<const void*>(kernel), SplitSmem<MC>::kDynamic, done);
+    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), SplitSmem<MC>::kDynamic);
     if (err != cudaSuccess) return err;
     CUtensorMap tx, tw;
     if (!make_tmap_i8(&tx, a.x, a.M, a.K, MC) || !make_tmap_i8(&tw, a.w, a.N, a.K, kRows))
@@ -764,9 +754,8 @@ cudaError_t launch_split(const LinearI8Args& a, int splits, cudaStream_t stream)
 
 template <int TN, typename YT>
 cudaError_t launch_pair(const LinearI8Args& a, cudaStream_t stream) {
-    static std::atomic<bool> done[kDevs];
     const auto kernel = linear_i8_pair_kernel<TN, YT>;
-    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), PairSmem<TN>::kDynamic, done);
+    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), PairSmem<TN>::kDynamic);
     if (err != cudaSuccess) return err;
     CUtensorMap tx, tw;
     if (!make_tmap_i8(&tx, a.x, a.M, a.K, 128) || !make_tmap_i8(&tw, a.w, a.N, a.K, TN / 2))
@@ -787,8 +776,9 @@ template <int MT, int R, int W, typename YT>
 cudaError_t launch_vec_r(const LinearI8Args& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     const int64_t rows = kVecThreads / 32 / W * R;
-    cfg.gridDim = dim3(static_cast<unsigned>((a.N + rows - 1) / rows),
-                       static_cast<unsigned>((a.M + MT - 1) / MT));
+    const int64_t n_blocks = (a.N + rows - 1) / rows, blocks = n_blocks * ((a.M + MT - 1) / MT);
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(kVecThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -798,7 +788,8 @@ cudaError_t launch_vec_r(const LinearI8Args& a, cudaStream_t stream) {
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, linear_i8_vec_kernel<MT, R, W, YT>, a.x, a.x_scale, a.w,
                               a.w_scale, static_cast<YT*>(a.y), static_cast<int>(a.M),
-                              static_cast<int>(a.N), static_cast<int>(a.K));
+                              static_cast<int>(a.N), static_cast<int>(a.K),
+                              static_cast<int>(n_blocks));
 }
 
 // W warps share a row so that long rows are on their way at once: at one

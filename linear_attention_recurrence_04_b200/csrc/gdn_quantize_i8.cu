@@ -426,6 +426,82 @@ cudaError_t launch_typed(const RowsI8Args& a, cudaStream_t stream) {
     }
 }
 
+// The layer's gated RMS norm (per value head, times norm_w and SiLU(z)) with
+// the whole position's row in 8-bit integers: sixteen threads a head, eight
+// elements a thread, a block a position. kKeep: every element of the row has
+// its thread (at most 64 heads); else the row is formed twice, once for its
+// maximum and once for its integers.
+template <bool kKeep>
+__global__ void __launch_bounds__(1024)
+gated_norm_i8_kernel(const float* __restrict__ o, const float* __restrict__ z,
+                     const float* __restrict__ norm_w, float eps, int8_t* __restrict__ q,
+                     float* __restrict__ scale, int n_groups) {
+    __shared__ uint32_t s_max[32];
+    tc::grid_dep_launch();
+    tc::grid_dep_wait();
+    const int T = blockDim.x;                       // a multiple of 32
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * n_groups * kVec;
+    const int col = static_cast<int>(threadIdx.x % 16) * kVec;
+    float w[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) w[i] = norm_w[col + i];
+    // y of a group (zeros past the row: every lane takes part in the sums)
+    auto form = [&](int g, float (&y)[kVec]) {
+        Raw<float> orr, zrr;
+        float zv[kVec];
+        const int64_t at = base + static_cast<int64_t>(g < n_groups ? g : 0) * kVec;
+        orr.load(o + at);
+        zrr.load(z + at);
+        orr.unpack(y);
+        zrr.unpack(zv);
+        double ss = 0.0;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            ss = fma(static_cast<double>(y[i]), static_cast<double>(y[i]), ss);
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(kFull, ss, off);
+        const float inv = static_cast<float>(
+            1.0 / sqrt(ss / static_cast<double>(kDv) + static_cast<double>(eps)));
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            y[i] = g < n_groups ? y[i] * inv * w[i] * siluf_acc(zv[i]) : 0.0f;
+    };
+    float y[kVec];
+    float top = 0.0f;
+    for (int g0 = 0; g0 < n_groups; g0 += T) {
+        form(g0 + threadIdx.x, y);
+#pragma unroll
+        for (int i = 0; i < kVec; i += 2) top = max_abs(top, y[i], y[i + 1]);
+    }
+    uint32_t mbits = __reduce_max_sync(kFull, __float_as_uint(top));
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) s_max[threadIdx.x >> 5] = mbits;
+    __syncthreads();
+    mbits = __reduce_max_sync(kFull, lane < (T >> 5) ? s_max[lane] : 0u);
+    const float m = __uint_as_float(mbits);
+    const bool plain = m >= kLow && m <= kHigh;
+    const float r = __fdiv_rn(127.0f, m);
+    for (int g0 = 0; g0 < n_groups; g0 += T) {
+        const int g = g0 + threadIdx.x;
+        if constexpr (!kKeep) form(g, y);
+        if (g < n_groups) {
+            int8_t* dst = q + base + static_cast<int64_t>(g) * kVec;
+            if (plain) {
+                float far = 0.0f;
+                *reinterpret_cast<uint2*>(dst) = quantize8(y, r, far);
+                if (far > kNear)
+                    decide8(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], m, r, dst);
+            } else {
+                rare8(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], mbits, dst);
+            }
+        }
+        __syncwarp();
+    }
+    if (threadIdx.x == 0)
+        scale[blockIdx.x] = mbits >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                                                 : static_cast<float>(static_cast<double>(m) / 127.0);
+}
+
 }  // namespace
 
 cudaError_t launch_rows_i8(const RowsI8Args& a, cudaStream_t stream) {
@@ -439,6 +515,23 @@ cudaError_t launch_rows_i8(const RowsI8Args& a, cudaStream_t stream) {
                                : launch_typed<bf16, float, true>(a, stream);
     return a.residual_bf16 ? launch_typed<float, bf16, true>(a, stream)
                            : launch_typed<float, float, true>(a, stream);
+}
+
+cudaError_t launch_gated_norm_i8(const GatedNormI8Args& a, cudaStream_t stream) {
+    if (a.M == 0) return cudaSuccess;
+    const int groups = a.Hv * (kDv / kVec);
+    const int threads = std::min(1024, (groups + 31) / 32 * 32);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.M));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const auto kernel = groups <= 1024 ? gated_norm_i8_kernel<true> : gated_norm_i8_kernel<false>;
+    return cudaLaunchKernelEx(&cfg, kernel, a.o, a.z, a.norm_w, a.eps, a.q, a.scale, groups);
 }
 
 }  // namespace gdn

@@ -35,7 +35,7 @@ EXPORTS = ("gdn_status_string", "gdn_last_error", "gdn_last_cuda_error", "gdn_st
            "gdn_forward_batch", "gdn_forward_batch_noalloc", "gdn_short_conv_workspace_size",
            "gdn_short_conv_forward_batch", "gdn_short_conv_forward", "gdn_short_conv_pair",
            "gdn_kda_step", "gdn_kda_prefill", "gdn_quantize_i8", "gdn_add_rms_norm_i8",
-           "gdn_linear_i8", "gdn_selftest_bounded_wait",
+           "gdn_linear_i8", "gdn_forward_batch_i8", "gdn_selftest_bounded_wait",
            "gdn_selftest_grid_barrier")
 
 
@@ -104,6 +104,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                         + [_VP, _VP, _I64, _I64, _VP])
     lib.gdn_linear_i8.restype = ctypes.c_int
     lib.gdn_linear_i8.argtypes = [_VP] * 5 + [ctypes.c_int] + [_I64] * 3 + [_VP, _VP]
+    lib.gdn_forward_batch_i8.restype = ctypes.c_int
+    lib.gdn_forward_batch_i8.argtypes = ([_VP] * 15 + [_F32, _F32] + [_VP, _VP, ctypes.c_int]
+                                         + [_VP, ctypes.c_size_t] + [_I64] * 8 + [_VP, _VP])
     lib.gdn_selftest_bounded_wait.restype = ctypes.c_int
     lib.gdn_selftest_bounded_wait.argtypes = [_VP, ctypes.c_uint64, ctypes.c_int, _VP]
     lib.gdn_selftest_grid_barrier.restype = ctypes.c_int
@@ -604,6 +607,14 @@ def _launch(fn, name, dev, args, stream):
         _raise_on(name, status)
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor that belongs to the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 # The three calls below are short on the device (2 to 10 us at decode sizes),
 # so what is right is recognised in one expression and everything else left to
 # the checks that name what is wrong.
@@ -643,9 +654,9 @@ def quantize_i8(x, q=None, scale=None, *, stream=None):
     if not good:
         _rows_i8_refuse(x, q, scale)
     if q is None:
-        q = torch.empty(shape, dtype=torch.int8, device=x.device)
+        q = _empty(shape, torch.int8, x.device, stream)
     if scale is None:
-        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+        scale = _empty(lead, torch.float32, x.device, stream)
     _launch(load_library().gdn_quantize_i8, "gdn_quantize_i8", dev,
             (x.data_ptr(), _DTYPES[dtype], q.data_ptr(), scale.data_ptr(), M, D), stream)
     return q, scale
@@ -682,11 +693,11 @@ def add_rms_norm_i8(x, weight, residual=None, residual_out=None, q=None, scale=N
     if not good:
         _rows_i8_refuse(x, q, scale, weight, residual, residual_out)
     if q is None:
-        q = torch.empty(shape, dtype=torch.int8, device=x.device)
+        q = _empty(shape, torch.int8, x.device, stream)
     if scale is None:
-        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+        scale = _empty(lead, torch.float32, x.device, stream)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = _empty(shape, rdtype, x.device, stream)
     _launch(load_library().gdn_add_rms_norm_i8, "gdn_add_rms_norm_i8", dev,
             (x.data_ptr(), _DTYPES[dtype], None if residual is None else residual.data_ptr(),
              weight.data_ptr(), eps, None if residual_out is None else residual_out.data_ptr(),
@@ -735,7 +746,7 @@ def linear_i8(x, x_scale, w, w_scale, y=None, *, out_dtype=torch.float32, status
     if y is None:
         if out_dtype not in _DTYPES:
             raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
-        y = torch.empty((*lead, N), dtype=out_dtype, device=x.device)
+        y = _empty((*lead, N), out_dtype, x.device, stream)
     sp = None
     if status is not None:
         if status.dtype is not torch.int32 or status.device != x.device or status.numel() != 1:
@@ -745,6 +756,64 @@ def linear_i8(x, x_scale, w, w_scale, y=None, *, out_dtype=torch.float32, status
             (x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), y.data_ptr(),
              _DTYPES[y.dtype], M, N, K, sp), stream)
     return y
+
+
+def forward_batch_i8(hidden, hidden_scale, w_qkv, s_qkv, w_z, s_z, w_ba, s_ba, w_out, s_out,
+                     conv_ring, conv_w, A_log, dt_bias, norm_w, state, out=None, workspace=None, *,
+                     Hk: int, l2_eps: float = 1e-6, norm_eps: float = 1e-6,
+                     out_dtype=torch.float32, status=None, stream=None):
+    """forward_batch with 8-bit projections: hidden [B, T, D] int8 with
+    hidden_scale [B, T] (from add_rms_norm_i8 or quantize_i8), weights as
+    forward_batch's but int8 with a scale a row (from quantize_i8). Returns out
+    [B, T, D] of `out_dtype` (fp32 or bf16), or of its own type when given."""
+    if not isinstance(hidden, torch.Tensor) or hidden.dim() != 3:
+        raise ValueError("hidden must be [B, T, D]")
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be [B, Hv, dv, dk]")
+    if not isinstance(conv_w, torch.Tensor) or conv_w.dim() != 2:
+        raise ValueError("conv_w must be [C, K]")
+    B, T, D = hidden.shape
+    Hv, dv, dk = state.shape[1:]
+    C, K = conv_w.shape
+    dev = hidden.get_device()
+    for t, name, dtypes, shape in (
+            (hidden, "hidden", _I8_ONLY, (B, T, D)), (hidden_scale, "hidden_scale", _F32_ONLY, (B, T)),
+            (w_qkv, "w_qkv", _I8_ONLY, (C, D)), (s_qkv, "s_qkv", _F32_ONLY, (C,)),
+            (w_z, "w_z", _I8_ONLY, (Hv * dv, D)), (s_z, "s_z", _F32_ONLY, (Hv * dv,)),
+            (w_ba, "w_ba", _I8_ONLY, (2 * Hv, D)), (s_ba, "s_ba", _F32_ONLY, (2 * Hv,)),
+            (w_out, "w_out", _I8_ONLY, (D, Hv * dv)), (s_out, "s_out", _F32_ONLY, (D,)),
+            (conv_ring, "conv_ring", _F32_ONLY, (B, K - 1, C)), (conv_w, "conv_w", _F32_ONLY, (C, K)),
+            (A_log, "A_log", _F32_ONLY, (Hv,)), (dt_bias, "dt_bias", _F32_ONLY, (Hv,)),
+            (norm_w, "norm_w", _F32_ONLY, (dv,)), (state, "state", _F32_ONLY, (B, Hv, dv, dk))):
+        _check(t, name, dtypes, shape, dev)
+    if C != 2 * Hk * dk + Hv * dv:
+        raise ValueError(f"conv_w has {C} channels, expected {2 * Hk * dk + Hv * dv}")
+    device = hidden.device
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+        out = _empty((B, T, D), out_dtype, device, stream)
+    else:
+        _check(out, "out", _FLOATS, (B, T, D), dev)
+    lib = load_library()
+    need = int(lib.gdn_forward_batch_workspace_size(B, T, Hk, Hv, dk, dv))
+    if workspace is None:
+        workspace = _empty((max(need, 1),), torch.uint8, device, stream)
+    if workspace.dtype is not torch.uint8 or workspace.device != device:
+        raise TypeError("workspace must be a uint8 tensor on the same device")
+    sp = None
+    if status is not None:
+        if status.dtype is not torch.int32 or status.device != device or status.numel() != 1:
+            raise TypeError("status must be a one-element int32 tensor on the same device")
+        sp = status.data_ptr()
+    _launch(lib.gdn_forward_batch_i8, "gdn_forward_batch_i8", dev,
+            (hidden.data_ptr(), hidden_scale.data_ptr(), w_qkv.data_ptr(), s_qkv.data_ptr(),
+             w_z.data_ptr(), s_z.data_ptr(), w_ba.data_ptr(), s_ba.data_ptr(), w_out.data_ptr(),
+             s_out.data_ptr(), conv_ring.data_ptr(), conv_w.data_ptr(), A_log.data_ptr(),
+             dt_bias.data_ptr(), norm_w.data_ptr(), float(l2_eps), float(norm_eps),
+             state.data_ptr(), out.data_ptr(), _DTYPES[out.dtype], workspace.data_ptr(),
+             workspace.numel(), B, T, D, Hk, Hv, dk, dv, K, sp), stream)
+    return out
 
 
 # -- failure detection -------------------------------------------------------

@@ -348,3 +348,103 @@ def test_layer_decode_with_8_bit_projections():
     check_rows(qy, sy, *ref.rows(n(y))[:2])
     assert np.array_equal(n(out), ref.linear(qy.cpu().numpy(), n(sy), wq["w_out"][0].cpu().numpy(),
                                              n(wq["w_out"][1]), True))
+
+
+# -- the layer over positions ---------------------------------------------------------
+
+def layer_reference(d, Hk):
+    """What forward_batch_i8 gets and gives, from forward_inputs' arrays: the
+    integers and scales, the oracle's y [B, T, Hv*128] in 64 bits from the
+    exact projections, the ring and the state."""
+    B, T, D = d["hidden"].shape
+    qs = {k: ref.rows(d[k].reshape(-1, d[k].shape[-1]))[:2]
+          for k in ("hidden", "w_qkv", "w_z", "w_ba", "w_out")}
+    qs = {k: (q, s.astype(np.float32)) for k, (q, s) in qs.items()}
+    p = {k: ref.linear(*qs["hidden"], *qs[k]).reshape(B, T, -1) for k in ("w_qkv", "w_z", "w_ba")}
+    Hv = d["A_log"].shape[0]
+    o, ring, state = oracle.load(), d["conv_ring"], d["state"]
+    ys = []
+    for t in range(T):
+        c = lambda v: np.ascontiguousarray(v)  # noqa: E731
+        y, ring, state = o.layer_decode(c(p["w_qkv"][:, t]), c(p["w_z"][:, t]),
+                                        c(p["w_ba"][:, t, Hv:]), c(p["w_ba"][:, t, :Hv]), ring,
+                                        d["conv_w"], d["A_log"], d["dt_bias"], d["norm_w"], state,
+                                        Hk=Hk)
+        ys.append(y)
+    return qs, p, np.stack(ys, 1), ring, state
+
+
+def output_bound(y, wq, ws):
+    """out from y [R, HD] in 64 bits, and how far the call's may be from it. Its
+    y is within the parity tests' 1e-5 of this one, so its row maximum m is:
+    an integer that both give alike stands for values 127 e / m of itself
+    apart (e = 1e-5), and only where 127 y / m lies within 2 * 127 e / m of a
+    half may it be one step off. The product adds three roundings."""
+    e = 1e-5
+    m = np.abs(y).max(1, keepdims=True)
+    t = 127.0 * y / m
+    q = np.rint(t)
+    near = np.abs(np.abs(t - np.floor(t)) - 0.5) <= 2 * 127.0 * e / m
+    s = m / 127.0
+    w = wq.astype(np.float64) * ws.astype(np.float64)[:, None]
+    slack = np.abs(q) * s * (e / m + 2.0 ** -24) + near * s
+    out = (q * s) @ w.T
+    return out, slack @ np.abs(w).T + 3 * 2.0 ** -24 * np.abs(out)
+
+
+def run_layer(d, qs, Hk, out_dtype=F32, T=None, t0=0, ring=None, state=None):
+    dev = lambda v: torch.from_numpy(np.ascontiguousarray(v)).cuda()  # noqa: E731
+    B, Tall, D = d["hidden"].shape
+    T = Tall if T is None else T
+    hq, hs = qs["hidden"][0].reshape(B, Tall, D), qs["hidden"][1].reshape(B, Tall)
+    ring = dev(d["conv_ring"]) if ring is None else ring
+    state = dev(d["state"]) if state is None else state
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w = [dev(v) for k in ("w_qkv", "w_z", "w_ba", "w_out") for v in qs[k]]
+    out = gdn.forward_batch_i8(dev(hq[:, t0:t0 + T]), dev(hs[:, t0:t0 + T]), *w, ring,
+                               dev(d["conv_w"]), dev(d["A_log"]), dev(d["dt_bias"]),
+                               dev(d["norm_w"]), state, Hk=Hk, out_dtype=out_dtype, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    return out, ring, state
+
+
+@pytest.mark.parametrize("B,T,D,Hk,Hv,dtype", [
+    (2, 37, 256, 16, 32, F32), (1, 5, 64, 16, 32, BF16), (3, 1, 512, 16, 32, F32),
+    (2, 3, 48, 1, 1, F32), (1, 2, 64, 72, 72, BF16), (1, 70, 128, 2, 4, F32)])
+def test_forward_batch_i8(B, T, D, Hk, Hv, dtype):
+    d = inputs.forward_inputs(B, T, D=D, Hk=Hk, Hv=Hv, seed=2000 + B + T + Hv, state_std=0.05)
+    qs, p, y, ring_r, state_r = layer_reference(d, Hk)
+    out, ring, state = run_layer(d, qs, Hk, dtype)
+    want, bound = output_bound(y.reshape(B * T, -1), *qs["w_out"])
+    if dtype is BF16:
+        bound = bound + torch.finfo(BF16).eps / 2 * (np.abs(want) + bound)
+    got = out.double().cpu().numpy().reshape(B * T, D)
+    assert np.all(np.abs(got - want) <= bound), np.max(np.abs(got - want) / bound)
+    assert_parity(state.cpu().numpy(), state_r, "state")
+    # the ring holds raw projections: the exact ones
+    raw = np.concatenate([d["conv_ring"], p["w_qkv"]], 1)[:, -ring.shape[1]:]
+    assert np.array_equal(ring.cpu().numpy(), raw)
+
+
+def test_forward_batch_i8_chunks_and_empty():
+    """11 positions in one call and as 4 and 7 resumed from the ring and state
+    are both the reference's; a call of no positions does nothing."""
+    d = inputs.forward_inputs(2, 11, D=96, seed=2100, state_std=0.05)
+    qs, _, y, ring_r, state_r = layer_reference(d, 16)
+    want, bound = output_bound(y.reshape(22, -1), *qs["w_out"])
+    out, ring, state = run_layer(d, qs, 16)
+    a, r, s = run_layer(d, qs, 16, T=4)
+    b, r, s = run_layer(d, qs, 16, T=7, t0=4, ring=r, state=s)
+    for got, st in ((out, state), (torch.cat([a, b], 1), s)):
+        assert_parity(st.cpu().numpy(), state_r, "state")
+        assert np.all(np.abs(got.double().cpu().numpy().reshape(22, -1) - want) <= bound)
+    assert torch.equal(r, ring)
+    e, r2, s2 = run_layer(d, qs, 16, T=0, ring=r.clone(), state=s.clone())
+    assert e.shape == (2, 0, 96) and torch.equal(r2, r) and torch.equal(s2, s)
+
+
+def test_linear_many_short_rows():
+    """More tokens than a grid's second dimension has blocks of eight."""
+    check_product(600_001, 1, 16, BF16)
+    check_product(70_000, 9, 48, F32)

@@ -98,3 +98,24 @@ def test_definition():
     q, s, _ = ref.rows(x, None, w, 1e-6)
     want = x * w / np.sqrt(np.mean(x.astype(np.float64) ** 2, 1) + 1e-6)[:, None]
     assert (np.abs(q * s[:, None] - want) <= 0.5 * s[:, None] * (1 + 1e-6)).all()
+
+
+def test_forward_batch_i8_argument_checks(lib):
+    ws = lib.gdn_forward_batch_workspace_size(2, 3, 16, 32, 128, 128)
+
+    def f(hidden=fake(1), hs=fake(2), w_out=fake(9), D=64, out=fake(20), ot=0, workspace=fake(21),
+          bytes_=ws, K=4, Hv=32, B=2, T=3, norm_w=fake(15), st=0):
+        return lib.gdn_forward_batch_i8(hidden, hs, fake(3), fake(4), fake(5), fake(6), fake(7),
+                                        fake(8), w_out, fake(10), fake(11), fake(12), fake(13),
+                                        fake(14), norm_w, 1e-6, 1e-6, fake(16), out, ot, workspace,
+                                        bytes_, B, T, D, 16, Hv, 128, 128, K, st, None)
+    assert f(D=24) == UNSUP and f(D=0) == UNSUP and f(D=131072) == UNSUP and f(Hv=1024) == UNSUP
+    assert f(K=3) == UNSUP and f(ot=5) == UNSUP
+    assert f(T=-1) == SHAPE and f(Hv=20) == SHAPE and f(bytes_=ws - 1) == SHAPE
+    assert f(B=70000) == OVERFLOW
+    assert f(hidden=0) == NULL and f(hs=0) == NULL and f(out=0) == NULL and f(workspace=0) == NULL
+    assert f(hidden=fake(1) + 8) == ALIGN and f(workspace=fake(21) + 128) == ALIGN
+    assert f(norm_w=fake(15) + 2) == ALIGN and f(st=fake(22) + 1) == ALIGN
+    assert f(out=fake(21) + 256) == ALIAS and f(out=fake(1)) == ALIAS and f(out=fake(16)) == ALIAS
+    assert f(w_out=fake(11)) == ALIAS                       # the ring is updated in place
+    assert f(hidden=0, out=0, T=0) == OK
