@@ -56,36 +56,40 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
     *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(b);
 }
 
-// 32 bytes (a whole sector) at once, past L1: nothing here reads it again.
-__device__ __forceinline__ void store32b(void* p, const uint32_t (&u)[8]) {
-    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], "
-                 "{%1, %2, %3, %4, %5, %6, %7, %8};"
+// 16 or 32 bytes at once (32: a whole sector), past L1: nothing here reads it
+// again.
+__device__ __forceinline__ void store16b(void* p, const uint32_t* u) {
+    asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};"
+                 ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
+}
+__device__ __forceinline__ void store32b(void* p, const uint32_t* u) {
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                  ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]),
                    "r"(u[6]), "r"(u[7]) : "memory");
 }
-__device__ __forceinline__ uint32_t bits2(float a, float b) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&p);
-}
-// The first `n` (a whole number of 32-byte pieces) of a token's 32 channels.
-__device__ __forceinline__ void store32(float* p, const float (&v)[32], int n) {
+// The first `n` of a token's 32 channels, `align` (16 or 32) bytes at once: n
+// is a whole number of such pieces.
+template <typename YT>
+__device__ __forceinline__ void store32(YT* p, const float (&v)[32], int n, int align) {
+    constexpr int kWords = 32 * sizeof(YT) / 4, kPer = 4 / sizeof(YT);   // channels a word
+    uint32_t u[kWords];
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-        const uint32_t u[8] = {__float_as_uint(v[j]),     __float_as_uint(v[j + 1]),
-                               __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3]),
-                               __float_as_uint(v[j + 4]), __float_as_uint(v[j + 5]),
-                               __float_as_uint(v[j + 6]), __float_as_uint(v[j + 7])};
-        if (j < n) store32b(p + j, u);
+    for (int j = 0; j < kWords; ++j) {
+        if constexpr (sizeof(YT) == 4) {
+            u[j] = __float_as_uint(v[j]);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            u[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
     }
-}
-__device__ __forceinline__ void store32(__nv_bfloat16* p, const float (&v)[32], int n) {
+    if (align == 32) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 16) {
-        const uint32_t u[8] = {bits2(v[j], v[j + 1]),       bits2(v[j + 2], v[j + 3]),
-                               bits2(v[j + 4], v[j + 5]),   bits2(v[j + 6], v[j + 7]),
-                               bits2(v[j + 8], v[j + 9]),   bits2(v[j + 10], v[j + 11]),
-                               bits2(v[j + 12], v[j + 13]), bits2(v[j + 14], v[j + 15])};
-        if (j < n) store32b(p + j, u);
+        for (int j = 0; j < kWords; j += 8)
+            if (j * kPer < n) store32b(p + j * kPer, u + j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kWords; j += 4)
+            if (j * kPer < n) store16b(p + j * kPer, u + j);
     }
 }
 // v[j] of lane i becomes v[i] of lane j: at each step the lanes that differ in
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
                       const __grid_constant__ CUtensorMap tmap_w,
                       const float* __restrict__ x_scale, const float* __restrict__ w_scale,
-                      YT* __restrict__ y, bool wide, int M, int N, int K,
+                      YT* __restrict__ y, int align, int M, int N, int K,
                       uint32_t* __restrict__ status) {
     using L = PairSmem<TN>;
     constexpr int kPairStages = L::kStages;
@@ -560,9 +564,9 @@ linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     v[j + 2] = scaled(static_cast<int>(r[j + 2]), sx, f.z);
                     v[j + 3] = scaled(static_cast<int>(r[j + 3]), sx, f.w);
                 }
-                if (wide) {
+                if (align >= 16) {
                     if (row < M)
-                        store32(y + static_cast<int64_t>(row) * N + n0 + c0, v, channels - c0);
+                        store32(y + static_cast<int64_t>(row) * N + n0 + c0, v, channels - c0, align);
                 } else {
                     // rows that are not aligned: one token's 32 channels a store
                     transpose32(v, lane);
@@ -766,9 +770,10 @@ cudaError_t launch_pair(const LinearI8Args& a, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(static_cast<unsigned>(2 * pairs), kPairThreads, 2,
                                                   PairSmem<TN>::kDynamic, stream, attr);
+    const uint64_t rows = (a.N * sizeof(YT)) | reinterpret_cast<uintptr_t>(a.y);   // their alignment
     return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a.x_scale, a.w_scale,
                               static_cast<YT*>(a.y),
-                              ((a.N * sizeof(YT)) | reinterpret_cast<uintptr_t>(a.y)) % 32 == 0, static_cast<int>(a.M),
+                              rows % 32 == 0 ? 32 : rows % 16 == 0 ? 16 : 0, static_cast<int>(a.M),
                               static_cast<int>(a.N), static_cast<int>(a.K), a.status);
 }
 
