@@ -558,6 +558,7 @@ linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
 #pragma unroll
             for (int j = 0; j < TN / 2; j += 32)
                 sws[j + lane] = j + lane < channels ? w_scale[n0 + j + lane] : 0.0f;
+            __syncwarp();
             const uint32_t src = tmem + static_cast<uint32_t>(acc) * TN + col0 +
                                  (static_cast<uint32_t>(quarter * 32) << 16);
             if (!tc::mbar_wait_warp(tc::smem_u32(&acc_full[acc]), (li >> 1) & 1)) {

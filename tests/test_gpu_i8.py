@@ -149,6 +149,33 @@ def test_borders():
     assert (ref.rows(x)[0][0, 1:128] == np.rint(np.arange(127) + 0.5)).all()
 
 
+def test_every_bf16_quotient():
+    """Rows of bf16 values with every pair of 8-bit mantissas at every distance
+    of exponents that leaves an integer but zero: all their halves are exact."""
+    a = torch.arange(128, 256, dtype=F32)
+    a = torch.cat([a * 2.0 ** -s for s in range(9)])
+    a = torch.cat([a, -a, torch.zeros(16 - (2 * a.numel() + 1) % 16)])
+    x = torch.stack([torch.cat([torch.tensor([float(m)]), torch.where(a.abs() <= m, a, 0 * a)])
+                     for m in range(128, 256)])
+    for scale in (1.0, 2.0 ** -60, 2.0 ** -110, 2.0 ** 112, 2.0 ** 120):
+        xb = (x * scale).to(BF16)
+        assert torch.equal(xb.double(), x.double() * scale)
+        want = ref.rows(xb.float().numpy())
+        for t in (xb, xb.float()):
+            check_rows(*gdn.quantize_i8(t.cuda()), *want[:2])
+
+
+@pytest.mark.parametrize("M,D", [(3, 2048), (2, 32784)])
+def test_residual_without_its_output(M, D):
+    """The C entry point takes a residual and leaves residual_out out."""
+    x, r, w = draw_rows(M, D, 1).cuda(), draw_rows(M, D, 2, BF16).cuda(), torch.ones(D, device="cuda")
+    q, s = torch.empty(M, D, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    assert gdn.load_library().gdn_add_rms_norm_i8(
+        x.data_ptr(), 0, r.data_ptr(), w.data_ptr(), 1e-6, None, 1, q.data_ptr(), s.data_ptr(), M, D,
+        torch.cuda.current_stream().cuda_stream) == 0
+    check_rows(q, s, *ref.rows(x.cpu().numpy(), r.float().cpu().numpy(), np.ones(D), residual_bf16=True)[:2])
+
+
 def test_rows_independent_of_batch():
     x = draw_rows(1000, 2048, 9).cuda()
     q, s = gdn.quantize_i8(x)
@@ -203,6 +230,23 @@ def test_linear_pair_tiles_ragged(dtype):
     """Enough tiles for every pair of SMs, no size on the tile grid."""
     check_product(2500, 2602, 400, dtype)
     check_product(2501, 2603, 16, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", [(3, 64, 256), (40, 256, 512), (70, 128, 4096), (2500, 2560, 272),
+                                   (2500, 2600, 144), (2500, 2564, 144)])
+def test_linear_output_of_least_alignment(M, N, K, dtype):
+    """y, x and w begin 16 bytes past a larger boundary, the scales 4."""
+    x, sx, w, sw = draw_product(M, N, K, M + N)
+    off = lambda t, n: torch.cat([t.new_zeros(n), t.reshape(-1)]).cuda()[n:].view(t.shape)  # noqa: E731
+    buf = torch.full((M * N + 40,), 7.0, dtype=dtype, device="cuda")
+    n = 16 // buf.element_size()
+    y = buf[n:n + M * N].view(M, N)
+    gdn.linear_i8(off(x, 16), off(sx, 1), off(w, 16), off(sw, 1), y)
+    torch.cuda.synchronize()
+    want = ref.linear(x.numpy(), sx.numpy(), w.numpy(), sw.numpy(), dtype is BF16)
+    assert np.array_equal(y.float().cpu().numpy(), want)
+    assert (buf[:n] == 7).all() and (buf[n + M * N:] == 7).all()
 
 
 def test_linear_large_sampled():
