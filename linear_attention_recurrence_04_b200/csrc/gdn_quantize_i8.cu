@@ -22,8 +22,8 @@
 // Bound by HBM for many rows: 16384 x 2048 fp32 with an fp32 residual 66.7 us
 // (6.5 TB/s of the 6.46 a copy reaches), 16384 x 4096 fp32 quantised 49.9 us;
 // bf16 rows, with half the bytes for the same instructions, 40.0 us for
-// 16384 x 2048 with a bf16 residual (5.9 TB/s) and 12.5 us for 8192 x 2048
-// quantised (4.0 TB/s; some 2 us of that is the launch's start and end). Few
+// 16384 x 2048 with a bf16 residual (5.9 TB/s) and 12.0 us for 8192 x 2048
+// quantised (4.2 TB/s; some 2 us of that is the launch's start and end). Few
 // rows are bound by latency: one row of 2048 takes 1.9 us. Rows fetched ahead
 // by persistent blocks (the next row's loads in registers) were slower: 12.7
 // and 55 us for the two bf16 shapes, for want of registers.
@@ -103,6 +103,34 @@ __device__ __forceinline__ float max_abs(float top, float a, float b) {
 constexpr float kNear = 0.5f - 0x1p-16f;
 constexpr float kMagic = 12582912.0f;           // 1.5 * 2^23: a sum's low bits are rint
 
+// Two fp32 values in a 64-bit register and the packed operations on them: each
+// an issue slot for both. bf16 rows are bound by issue (30000 x 1024 in 18.5
+// us against 19.6); for the fp32 norm the registers that they pair cost more
+// (16384 x 2048 in 70.8 against 66.7).
+struct F2 {
+    uint64_t v;
+    __device__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ explicit F2(uint64_t u) : v(u) {}
+    __device__ void get(float& a, float& b) const {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    }
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+    return F2(r);
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+    return F2(r);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return F2(r);
+}
+
 __device__ __forceinline__ uint2 low_bytes(const uint32_t (&b)[kVec]) {
     uint2 o;
     o.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
@@ -119,11 +147,15 @@ __device__ __forceinline__ uint2 low_bytes(const uint32_t (&b)[kVec]) {
 // unit of the 16 bits they have), and a half is hit exactly.
 __device__ __forceinline__ uint2 quantize8_bf16(const float (&a)[kVec], float m, float ri) {
     uint32_t b[kVec];
+    const F2 minus_m(-m, -m), ri2(ri, ri), c127(127.0f, 127.0f), magic(kMagic, kMagic);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        const float p = __fmul_rn(a[i], 127.0f);
-        const float t = __fmul_rn(p, ri);
-        b[i] = __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-t, m, p), ri, t), kMagic));
+    for (int i = 0; i < kVec; i += 2) {
+        const F2 p = mul2(F2(a[i], a[i + 1]), c127);
+        const F2 t = mul2(p, ri2);
+        float s0, s1;
+        add2(fma2(fma2(t, minus_m, p), ri2, t), magic).get(s0, s1);
+        b[i] = __float_as_uint(s0);
+        b[i + 1] = __float_as_uint(s1);
     }
     return low_bytes(b);
 }
@@ -370,11 +402,14 @@ quantize_rows_kernel(const XT* __restrict__ x, const RT* residual, const float* 
         }
     }
     if (threadIdx.x == 0) {
-        double s = static_cast<double>(m) / 127.0;
+        float s;
         if constexpr (kNorm)
-            s /= sqrt(sum / static_cast<double>(D) + static_cast<double>(eps));
-        scale[row] = mbits == 0u ? 0.0f : mbits >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                                               : static_cast<float>(s);
+            s = static_cast<float>(static_cast<double>(m) /
+                                   (127.0 * sqrt(sum / static_cast<double>(D) +
+                                                 static_cast<double>(eps))));
+        else
+            s = __fdiv_rn(m, 127.0f);
+        scale[row] = mbits == 0u ? 0.0f : mbits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : s;
     }
 }
 
@@ -508,7 +543,7 @@ gated_norm_i8_kernel(const float* __restrict__ o, const float* __restrict__ z,
     }
     if (threadIdx.x == 0)
         scale[blockIdx.x] = mbits >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                                 : static_cast<float>(static_cast<double>(m) / 127.0);
+                                                 : __fdiv_rn(m, 127.0f);
 }
 
 }  // namespace
