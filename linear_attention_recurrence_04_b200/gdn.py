@@ -164,13 +164,18 @@ def _ptr(t: torch.Tensor) -> int:
     return t.data_ptr() if t.numel() else 0
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
+
+
 def _stream(device: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
     if stream is not None:
         return stream.cuda_stream
     # torch.cuda.current_stream(device).cuda_stream without the Stream object
     # (0.2 against 2.3 us a call)
-    index = device.index if device.index is not None else torch.cuda.current_device()
-    return torch._C._cuda_getCurrentRawStream(index)
+    return _raw_stream(device.index if device.index is not None else torch.cuda.current_device())
 
 
 def step(state, q, k, v, beta, gate, out=None, *, stream=None):
@@ -562,6 +567,7 @@ def short_conv_pair(hidden, w_in, w_out, conv_ring, scratch_ring, conv_w, out=No
 # -- 8-bit projections ---------------------------------------------------------
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}    # gdn_dtype
+_I8, _F32T = torch.int8, torch.float32
 _F32_ONLY, _I8_ONLY, _FLOATS = (torch.float32,), (torch.int8,), (torch.float32, torch.bfloat16)
 
 
@@ -596,16 +602,15 @@ def _lead(t):
     return shape[:-1], shape[:-1].numel()
 
 
-def _launch(fn, name, dev, args, stream):
-    """Call `fn` with device number `dev` current on `stream`."""
-    st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
-    if torch._C._cuda_getDevice() == dev:
-        status = fn(*args, st)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, st)
-    if status:
-        _raise_on(name, status)
+def _enter(dev, stream):
+    """The handle of `stream` (of device number `dev`'s current one), and the
+    device to go back to after a call on `dev` (None: it is current)."""
+    handle = stream.cuda_stream if stream is not None else _raw_stream(dev)
+    current = _current_device()
+    if current == dev:
+        return handle, None
+    torch.cuda.set_device(dev)
+    return handle, current
 
 
 def _empty(shape, dtype, device, stream):
@@ -646,9 +651,9 @@ def quantize_i8(x, q=None, scale=None, *, stream=None):
         D = shape[-1]
         lead, M = _lead(x)
         good = (dev >= 0 and dtype in _DTYPES and x.is_contiguous()
-                and (q is None or (q.dtype is torch.int8 and q.shape == shape
+                and (q is None or (q.dtype is _I8 and q.shape == shape
                                    and q.get_device() == dev and q.is_contiguous()))
-                and (scale is None or (scale.dtype is torch.float32 and scale.shape == lead
+                and (scale is None or (scale.dtype is _F32T and scale.shape == lead
                                        and scale.get_device() == dev and scale.is_contiguous())))
     except (AttributeError, IndexError):
         good = False
@@ -658,8 +663,15 @@ def quantize_i8(x, q=None, scale=None, *, stream=None):
         q = _empty(shape, torch.int8, x.device, stream)
     if scale is None:
         scale = _empty(lead, torch.float32, x.device, stream)
-    _launch(load_library().gdn_quantize_i8, "gdn_quantize_i8", dev,
-            (x.data_ptr(), _DTYPES[dtype], q.data_ptr(), scale.data_ptr(), M, D), stream)
+    fn = load_library().gdn_quantize_i8
+    handle, back = _enter(dev, stream)
+    try:
+        st = fn(x.data_ptr(), _DTYPES[dtype], q.data_ptr(), scale.data_ptr(), M, D, handle)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if st:
+        _raise_on("gdn_quantize_i8", st)
     return q, scale
 
 
@@ -677,7 +689,7 @@ def add_rms_norm_i8(x, weight, residual=None, residual_out=None, q=None, scale=N
         rdtype = (residual.dtype if residual is not None else
                   residual_out.dtype if residual_out is not None else torch.float32)
         good = (dev >= 0 and dtype in _DTYPES and rdtype in _DTYPES and x.is_contiguous()
-                and weight.dtype is torch.float32 and weight.shape == (D,)
+                and weight.dtype is _F32T and weight.shape == (D,)
                 and weight.get_device() == dev and weight.is_contiguous()
                 and (residual is None or (residual.shape == shape and residual.get_device() == dev
                                           and residual.is_contiguous()))
@@ -685,9 +697,9 @@ def add_rms_norm_i8(x, weight, residual=None, residual_out=None, q=None, scale=N
                                               and residual_out.shape == shape
                                               and residual_out.get_device() == dev
                                               and residual_out.is_contiguous()))
-                and (q is None or (q.dtype is torch.int8 and q.shape == shape
+                and (q is None or (q.dtype is _I8 and q.shape == shape
                                    and q.get_device() == dev and q.is_contiguous()))
-                and (scale is None or (scale.dtype is torch.float32 and scale.shape == lead
+                and (scale is None or (scale.dtype is _F32T and scale.shape == lead
                                        and scale.get_device() == dev and scale.is_contiguous())))
     except (AttributeError, IndexError):
         good = False
@@ -699,10 +711,17 @@ def add_rms_norm_i8(x, weight, residual=None, residual_out=None, q=None, scale=N
         scale = _empty(lead, torch.float32, x.device, stream)
     if residual is not None and residual_out is None:
         residual_out = _empty(shape, rdtype, x.device, stream)
-    _launch(load_library().gdn_add_rms_norm_i8, "gdn_add_rms_norm_i8", dev,
-            (x.data_ptr(), _DTYPES[dtype], None if residual is None else residual.data_ptr(),
-             weight.data_ptr(), eps, None if residual_out is None else residual_out.data_ptr(),
-             _DTYPES[rdtype], q.data_ptr(), scale.data_ptr(), M, D), stream)
+    fn = load_library().gdn_add_rms_norm_i8
+    handle, back = _enter(dev, stream)
+    try:
+        st = fn(x.data_ptr(), _DTYPES[dtype], None if residual is None else residual.data_ptr(),
+                weight.data_ptr(), eps, None if residual_out is None else residual_out.data_ptr(),
+                _DTYPES[rdtype], q.data_ptr(), scale.data_ptr(), M, D, handle)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if st:
+        _raise_on("gdn_add_rms_norm_i8", st)
     return q, scale, residual_out
 
 
@@ -732,8 +751,8 @@ def linear_i8(x, x_scale, w, w_scale, y=None, *, out_dtype=torch.float32, status
         N, K = w.shape
         lead, M = _lead(x)
         dev = x.get_device()
-        good = (dev >= 0 and x.dtype is torch.int8 and w.dtype is torch.int8
-                and x_scale.dtype is torch.float32 and w_scale.dtype is torch.float32
+        good = (dev >= 0 and x.dtype is _I8 and w.dtype is _I8
+                and x_scale.dtype is _F32T and w_scale.dtype is _F32T
                 and x.shape[-1] == K and x_scale.shape == lead and w_scale.shape == (N,)
                 and w.get_device() == dev and x_scale.get_device() == dev
                 and w_scale.get_device() == dev and x.is_contiguous() and w.is_contiguous()
@@ -753,9 +772,16 @@ def linear_i8(x, x_scale, w, w_scale, y=None, *, out_dtype=torch.float32, status
         if status.dtype is not torch.int32 or status.device != x.device or status.numel() != 1:
             raise TypeError("status must be a one-element int32 tensor on the same device")
         sp = status.data_ptr()
-    _launch(load_library().gdn_linear_i8, "gdn_linear_i8", dev,
-            (x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), y.data_ptr(),
-             _DTYPES[y.dtype], M, N, K, sp), stream)
+    fn = load_library().gdn_linear_i8
+    handle, back = _enter(dev, stream)
+    try:
+        st = fn(x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), y.data_ptr(),
+                _DTYPES[y.dtype], M, N, K, sp, handle)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if st:
+        _raise_on("gdn_linear_i8", st)
     return y
 
 
@@ -807,13 +833,20 @@ def forward_batch_i8(hidden, hidden_scale, w_qkv, s_qkv, w_z, s_z, w_ba, s_ba, w
         if status.dtype is not torch.int32 or status.device != device or status.numel() != 1:
             raise TypeError("status must be a one-element int32 tensor on the same device")
         sp = status.data_ptr()
-    _launch(lib.gdn_forward_batch_i8, "gdn_forward_batch_i8", dev,
-            (hidden.data_ptr(), hidden_scale.data_ptr(), w_qkv.data_ptr(), s_qkv.data_ptr(),
+    handle, back = _enter(dev, stream)
+    try:
+        st = lib.gdn_forward_batch_i8(
+            hidden.data_ptr(), hidden_scale.data_ptr(), w_qkv.data_ptr(), s_qkv.data_ptr(),
              w_z.data_ptr(), s_z.data_ptr(), w_ba.data_ptr(), s_ba.data_ptr(), w_out.data_ptr(),
              s_out.data_ptr(), conv_ring.data_ptr(), conv_w.data_ptr(), A_log.data_ptr(),
              dt_bias.data_ptr(), norm_w.data_ptr(), float(l2_eps), float(norm_eps),
              state.data_ptr(), out.data_ptr(), _DTYPES[out.dtype], workspace.data_ptr(),
-             workspace.numel(), B, T, D, Hk, Hv, dk, dv, K, sp), stream)
+             workspace.numel(), B, T, D, Hk, Hv, dk, dv, K, sp, handle)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if st:
+        _raise_on("gdn_forward_batch_i8", st)
     return out
 
 
