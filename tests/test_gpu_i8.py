@@ -492,3 +492,88 @@ def test_linear_many_short_rows():
     """More tokens than a grid's second dimension has blocks of eight."""
     check_product(600_001, 1, 16, BF16)
     check_product(70_000, 9, 48, F32)
+
+
+# -- shapes, streams, threads, far offsets ---------------------------------------------
+
+def test_leading_dimensions():
+    """Rows over any leading dimensions, none of them too, and none at all."""
+    x = draw_rows(6, 64, 41).cuda()
+    w, ws = gdn.quantize_i8(draw_rows(9, 64, 42).cuda())
+    q, s = gdn.quantize_i8(x)
+    y = gdn.linear_i8(q, s, w, ws)
+    q3, s3, h3 = gdn.add_rms_norm_i8(x.view(2, 3, 64), torch.ones(64, device="cuda"),
+                                     torch.zeros(2, 3, 64, device="cuda"))
+    assert torch.equal(q3.view(6, 64), q) and s3.shape == (2, 3) and torch.equal(h3.view(6, 64), x)
+    q3, s3 = gdn.quantize_i8(x.view(2, 3, 64))
+    assert torch.equal(gdn.linear_i8(q3, s3, w, ws), y.view(2, 3, 9))
+    q1, s1 = gdn.quantize_i8(x[4])
+    assert s1.shape == () and torch.equal(gdn.linear_i8(q1, s1, w, ws), y[4])
+    e, es = gdn.quantize_i8(x.new_zeros(2, 0, 64))
+    assert gdn.linear_i8(e, es, w, ws).shape == (2, 0, 9)
+    # one tensor as both operands
+    assert np.array_equal(gdn.linear_i8(w, ws, w, ws).cpu().numpy(),
+                          ref.linear(w.cpu().numpy(), ws.cpu().numpy(), w.cpu().numpy(), ws.cpu().numpy()))
+
+
+def test_outputs_made_on_the_calls_stream():
+    """With `stream`, everything the call makes belongs to that stream."""
+    x, w = draw_rows(300, 2048, 43).cuda(), draw_rows(700, 2048, 44).cuda()
+    wq, ws = gdn.quantize_i8(w)
+    want = gdn.linear_i8(*gdn.quantize_i8(x), wq, ws)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for _ in range(20):
+        q, s = gdn.quantize_i8(x, stream=st)
+        y = gdn.linear_i8(q, s, wq, ws, stream=st)
+        del q, s                                    # their memory may serve this stream again
+        st.synchronize()
+        assert torch.equal(y, want)
+
+
+def test_two_host_threads():
+    """Calls of several host threads, each on a stream of its own."""
+    import threading
+    shapes = [(3, 200, 512), (40, 1000, 1040), (300, 520, 256), (700, 2050, 272)]
+    args = [[t.cuda() for t in draw_product(*sh, seed=sum(sh))] for sh in shapes]
+    want = [gdn.linear_i8(*a) for a in args]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        for _ in range(50):
+            for a, w in zip(args[i:] + args[:i], want[i:] + want[:i]):
+                y = gdn.linear_i8(*a, stream=st)
+                st.synchronize()
+                if not torch.equal(y, w):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(shapes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_offsets_past_32_bits():
+    """Outputs and rows beyond 2^32 elements: the last ones, and the ones that
+    a 32-bit offset would have written."""
+    M, N, K = 530_000, 8208, 16
+    x, sx, w, sw = draw_product(8, N, K, 45)
+    xb = torch.zeros(M, K, dtype=torch.int8, device="cuda")
+    xb[-8:] = x.cuda()
+    sb = torch.ones(M, device="cuda")
+    sb[-8:] = sx.cuda()
+    y = gdn.linear_i8(xb, sb, w.cuda(), sw.cuda(), out_dtype=BF16)
+    assert np.array_equal(y[-8:].float().cpu().numpy(), ref.linear(x, sx, w, sw, True))
+    assert int(torch.count_nonzero(y[:-8])) == 0
+    del y, xb, sb
+    M, D = 1_050_000, 4096
+    xb = torch.zeros(M, D, dtype=BF16, device="cuda")
+    x = draw_rows(5, D, 46, BF16)
+    xb[-5:] = x.cuda()
+    q, s = gdn.quantize_i8(xb)
+    check_rows(q[-5:], s[-5:], *ref.rows(x.float().numpy())[:2])
+    assert int(torch.count_nonzero(q[:-5])) == 0 and int(torch.count_nonzero(s[:-5])) == 0
