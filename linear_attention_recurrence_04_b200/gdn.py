@@ -594,14 +594,6 @@ def _check(t, name, dtypes, shape, device):
         _refuse(t, name, dtypes, shape, device)
 
 
-def _lead(t):
-    """The leading sizes of t [..., D] and their product."""
-    shape = t.shape
-    if len(shape) == 2:
-        return (shape[0],), shape[0]
-    return shape[:-1], shape[:-1].numel()
-
-
 def _enter(dev, stream):
     """The handle of `stream` (of device number `dev`'s current one), and the
     device to go back to after a call on `dev` (None: it is current)."""
@@ -648,8 +640,12 @@ def quantize_i8(x, q=None, scale=None, *, stream=None):
     channel. Returns (q [..., D] int8, scale [...] fp32), q * scale ~ x."""
     try:
         shape, dev, dtype = x.shape, x.get_device(), x.dtype
-        D = shape[-1]
-        lead, M = _lead(x)
+        if len(shape) == 2:
+            M, D = shape
+            lead = (M,)
+        else:
+            lead, D = shape[:-1], shape[-1]
+            M = lead.numel()
         good = (dev >= 0 and dtype in _DTYPES and x.is_contiguous()
                 and (q is None or (q.dtype is _I8 and q.shape == shape
                                    and q.get_device() == dev and q.is_contiguous()))
@@ -684,8 +680,12 @@ def add_rms_norm_i8(x, weight, residual=None, residual_out=None, q=None, scale=N
     `residual` is given). Returns (q, scale, residual_out or None)."""
     try:
         shape, dev, dtype = x.shape, x.get_device(), x.dtype
-        D = shape[-1]
-        lead, M = _lead(x)
+        if len(shape) == 2:
+            M, D = shape
+            lead = (M,)
+        else:
+            lead, D = shape[:-1], shape[-1]
+            M = lead.numel()
         rdtype = (residual.dtype if residual is not None else
                   residual_out.dtype if residual_out is not None else torch.float32)
         good = (dev >= 0 and dtype in _DTYPES and rdtype in _DTYPES and x.is_contiguous()
@@ -749,11 +749,17 @@ def linear_i8(x, x_scale, w, w_scale, y=None, *, out_dtype=torch.float32, status
     type when given. `status` as for linear_bf16."""
     try:
         N, K = w.shape
-        lead, M = _lead(x)
+        shape = x.shape
+        if len(shape) == 2:
+            M, depth = shape
+            lead = (M,)
+        else:
+            lead, depth = shape[:-1], shape[-1]
+            M = lead.numel()
         dev = x.get_device()
         good = (dev >= 0 and x.dtype is _I8 and w.dtype is _I8
                 and x_scale.dtype is _F32T and w_scale.dtype is _F32T
-                and x.shape[-1] == K and x_scale.shape == lead and w_scale.shape == (N,)
+                and depth == K and x_scale.shape == lead and w_scale.shape == (N,)
                 and w.get_device() == dev and x_scale.get_device() == dev
                 and w_scale.get_device() == dev and x.is_contiguous() and w.is_contiguous()
                 and x_scale.is_contiguous() and w_scale.is_contiguous()
