@@ -211,7 +211,7 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
         if (tc::elect_one()) {
             // the first weight boxes head for L2 while the previous kernel ends
             tc::tma_prefetch_l2_2d(&tmap_w, kb * kBK, n0);
-            tc::tma_prefetch_l2_2d(&tmap_w, kb * kBK + kAtom, n0);
+            if (kb * kBK + kAtom < K) tc::tma_prefetch_l2_2d(&tmap_w, kb * kBK + kAtom, n0);
         }
         tc::grid_dep_wait();
         int s = 0;
@@ -226,10 +226,13 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
             const uint32_t a = base + s * L::kStage;
             if (++s == kStages) { s = 0; ph ^= 1; }
             ready = tc::mbar_test_wait(tc::smem_u32(&empty[s]), ph);   // answered by the next pass
+            // (past the end of K nothing is loaded, and no MMA is issued)
+            const int left = K - kt * kBK;
             if (tc::elect_one()) {
-                tc::mbar_arrive_expect_tx(fb, L::kStage);
+                tc::mbar_arrive_expect_tx(fb, left > kAtom ? L::kStage : L::kW + L::kX);
 #pragma unroll
                 for (int i = 0; i < L::kAtoms; ++i) {
+                    if (i * kAtom >= left) continue;
                     tc::tma_load_2d(a + i * L::kW, &tmap_w, fb, kt * kBK + i * kAtom, n0);
                     tc::tma_load_2d(a + L::kAtoms * L::kW + i * L::kX, &tmap_x, fb,
                                     kt * kBK + i * kAtom, m0);
@@ -255,9 +258,11 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
             const uint32_t eb = tc::smem_u32(&empty[s]);
             if (++s == kStages) { s = 0; ph ^= 1; }
             ready = tc::mbar_test_wait(tc::smem_u32(&full[s]), ph);
+            const int left = K - kt * kBK;
             if (tc::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kBK / 32; ++kk) {    // 32 bytes on: addresses count 16s
+                    if (kk * 32 >= left) continue;
                     const int i = kk / 4, o = 2 * (kk % 4);
                     tc::mma_i8(tmem, a + (i * L::kW >> 4) + o, b + (i * L::kX >> 4) + o, idesc,
                                (kt > kb || kk > 0) ? 1u : 0u);
@@ -486,10 +491,14 @@ linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 const uint32_t own = tc::smem_u32(&full[s]);
                 if (++s == kPairStages) { s = 0; ph ^= 1; }
                 ready = tc::mbar_test_wait(tc::smem_u32(&empty[s]), ph);   // for the next pass
+                const int left = K - kt * kBK;
                 if (tc::elect_one()) {
-                    if (rank == 0) tc::mbar_arrive_expect_tx(own, 2 * L::kStage);
+                    if (rank == 0)
+                        tc::mbar_arrive_expect_tx(own, left > (L::kAtoms - 1) * kAtom
+                                                           ? 2 * L::kStage : 2 * (L::kX + L::kW));
 #pragma unroll
                     for (int i = 0; i < L::kAtoms; ++i) {
+                        if (i * kAtom >= left) continue;
                         const int k0 = kt * kBK + i * kAtom;
                         tc::tma_load_2d_pair(a + i * L::kX, &tmap_x, fb, k0, m0);
                         tc::tma_load_2d_pair(a + L::kAtoms * L::kX + i * L::kW, &tmap_w, fb, k0, n0);
@@ -527,9 +536,11 @@ linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
                 const uint32_t eb = tc::smem_u32(&empty[s]);
                 if (++s == kPairStages) { s = 0; ph ^= 1; }
                 ready = tc::mbar_test_wait(tc::smem_u32(&full[s]), ph);
+                const int left = K - kt * kBK;
                 if (tc::elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kBK / 32; ++kk) {
+                        if (kk * 32 >= left) continue;
                         const int i = kk / 4, o = 2 * (kk % 4);
                         tc::mma_i8_pair(d, a + (i * L::kX >> 4) + o, b + (i * L::kW >> 4) + o, idesc,
                                         (kt > 0 || kk > 0) ? 1u : 0u);
