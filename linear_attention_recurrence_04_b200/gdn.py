@@ -160,6 +160,14 @@ def _call(device: torch.device, fn, *args) -> int:
         return fn(*args)
 
 
+def _check_workspace(workspace: torch.Tensor, device: torch.device) -> None:
+    """The entry points get its address and numel() bytes from there."""
+    if workspace.dtype is not torch.uint8 or workspace.device != device:
+        raise TypeError("workspace must be a uint8 tensor on the same device")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _ptr(t: torch.Tensor) -> int:
     return t.data_ptr() if t.numel() else 0
 
@@ -385,8 +393,7 @@ def forward_batch(hidden, w_qkv, w_z, w_ba, w_out, conv_ring, conv_w, A_log, dt_
     need = forward_batch_workspace_size(B, T, Hk, Hv)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    if workspace.dtype is not torch.uint8 or workspace.device != device:
-        raise TypeError("workspace must be a uint8 tensor on the same device")
+    _check_workspace(workspace, device)
     expect = dict(w_qkv=(C, D), w_z=(Hv * 128, D), w_ba=(2 * Hv, D), w_out=(D, Hv * 128),
                   conv_ring=(B, K - 1, C), out=(B, T, D))
     for n, t in (("w_qkv", w_qkv), ("w_z", w_z), ("w_ba", w_ba), ("w_out", w_out),
@@ -508,8 +515,7 @@ def _short_conv_args(hidden, w_in, w_out, conv_ring, conv_w, out, workspace, T, 
     need = short_conv_workspace_size(B, T, D)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    if workspace.dtype is not torch.uint8 or workspace.device != device:
-        raise TypeError("workspace must be a uint8 tensor on the same device")
+    _check_workspace(workspace, device)
     return device, B, D, K, out, workspace
 
 
@@ -832,8 +838,7 @@ def forward_batch_i8(hidden, hidden_scale, w_qkv, s_qkv, w_z, s_z, w_ba, s_ba, w
     need = int(lib.gdn_forward_batch_workspace_size(B, T, Hk, Hv, dk, dv))
     if workspace is None:
         workspace = _empty((max(need, 1),), torch.uint8, device, stream)
-    if workspace.dtype is not torch.uint8 or workspace.device != device:
-        raise TypeError("workspace must be a uint8 tensor on the same device")
+    _check_workspace(workspace, device)
     sp = None
     if status is not None:
         if status.dtype is not torch.int32 or status.device != device or status.numel() != 1:
