@@ -298,7 +298,9 @@ gdn_status gdn_linear_bf16_split_k(const void *x, const void *w, float *y, int64
  *                no other way
  *   q [M][D] int8;  scale [M]
  * Both: D a multiple of 16, any size (rows of up to 32768 elements are read
- * once, longer ones twice). Results do not depend on M or on the other rows.
+ * once, longer ones twice; D = 0 gives scale = 0, and every other pointer,
+ * scale too, may then be NULL). Results do not depend on M or on the other
+ * rows.
  * All pointers 16-byte aligned, except scale (4). q and scale may overlap
  * nothing. M above 2^31 - 1 gives GDN_ERR_OVERFLOW; an unknown type
  * GDN_ERR_UNSUPPORTED.

@@ -438,7 +438,12 @@ gdn_status rows_i8_call(const char* fn, bool norm, const void* x, int x_type,
     int64_t n = 0;
     if (M > INT32_MAX || D > INT32_MAX || !mul_ok(M, D, &n) || n > INT64_MAX / 4)
         return fail(GDN_ERR_OVERFLOW, "%s: M or D too large", fn);
-    if (n == 0) { g_last_error[0] = '\0'; return GDN_OK; }
+    if (n == 0 && (M == 0 || !scale)) { g_last_error[0] = '\0'; return GDN_OK; }
+    if (n == 0) {    // rows of no elements: m = 0, scale = 0
+        if (!aligned(scale, 4)) return fail(GDN_ERR_ALIGN, "%s: alignment rule violated", fn);
+        return launched(cudaMemsetAsync(scale, 0, static_cast<size_t>(M) * 4,
+                                        static_cast<cudaStream_t>(stream)), fn);
+    }
     if (!x || !q || !scale || (norm && !weight))
         return fail(GDN_ERR_NULL, "%s: a tensor pointer is NULL", fn);
     if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4) || !aligned(residual, 16) ||

@@ -176,6 +176,18 @@ def test_residual_without_its_output(M, D):
     check_rows(q, s, *ref.rows(x.cpu().numpy(), r.float().cpu().numpy(), np.ones(D), residual_bf16=True)[:2])
 
 
+@pytest.mark.parametrize("M", [1, 4, 1000])
+def test_rows_of_no_elements(M):
+    """D = 0: the empty row's maximum is 0, so its scale is 0."""
+    x, w = torch.empty(M, 0, device="cuda"), torch.empty(0, device="cuda")
+    buf = torch.full((M + 1,), 7.0, device="cuda")
+    for call in (lambda: gdn.quantize_i8(x, scale=buf[:M]),
+                 lambda: gdn.add_rms_norm_i8(x.to(BF16), w, x, scale=buf[:M])):
+        buf.fill_(7.0)
+        call()
+        assert buf.tolist() == [0.0] * M + [7.0]
+
+
 def test_rows_independent_of_batch():
     x = draw_rows(1000, 2048, 9).cuda()
     q, s = gdn.quantize_i8(x)

@@ -63,6 +63,14 @@ def test_linear_i8_argument_checks(lib):
     assert f(x=0, w=0, y=0, M=0) == OK and f(x=0, w=0, y=0, N=0) == OK
 
 
+def test_rows_of_no_elements(lib):
+    """With D = 0 the scales are still written (as zeros), so their pointer is
+    held to its alignment; nothing else is looked at."""
+    assert lib.gdn_quantize_i8(0, 0, 0, fake(3) + 2, 4, 0, None) == ALIGN
+    assert lib.gdn_add_rms_norm_i8(0, 0, 0, 0, 1e-6, 0, 0, 0, fake(3) + 1, 4, 0, None) == ALIGN
+    assert lib.gdn_quantize_i8(0, 0, 0, fake(3) + 2, 0, 0, None) == OK
+
+
 def test_binding_refuses(lib):
     x = torch.zeros(4, 64)
     i = torch.zeros(4, 64, dtype=torch.int8)
