@@ -21,8 +21,12 @@ __device__ __forceinline__ float4 ld_stream(const float* p) {
 __device__ __forceinline__ void st_stream(float* p, float4 v) {
     __stcs(reinterpret_cast<float4*>(p), v);
 }
+// 16-byte load.
+__device__ __forceinline__ float4 ld4(const float* p) {
+    return *reinterpret_cast<const float4*>(p);
+}
 // Read-only 16-byte load through the non-coherent path (q, k, v rows that
-// many warps share).
+// many warps share), in kernels that start after the previous one's end.
 __device__ __forceinline__ float4 ld_ro4(const float* p) {
     return __ldg(reinterpret_cast<const float4*>(p));
 }

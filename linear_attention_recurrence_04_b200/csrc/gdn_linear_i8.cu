@@ -185,7 +185,7 @@ template <int MC, typename YT>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
                        const __grid_constant__ CUtensorMap tmap_w,
-                       const float* __restrict__ x_scale, const float* __restrict__ w_scale,
+                       const float* x_scale, const float* w_scale,
                        YT* __restrict__ y, int M, int N, int K, int splits,
                        uint32_t* __restrict__ status) {
     using L = SplitSmem<MC>;
@@ -195,6 +195,7 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
     __shared__ __align__(8) uint64_t empty[kStages];
     __shared__ __align__(8) uint64_t acc_full;
     __shared__ __align__(16) float sx_s[4][MC];        // the tokens' scales, for each epilogue warp
+    __shared__ __align__(16) float sw_s[kRows];        // the channels', for the cluster's sums
     __shared__ uint32_t tmem_slot;
     __shared__ int issued, consumed;
     __shared__ int failed;
@@ -312,9 +313,10 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
         const int tokens = min(MC, M - m0);
         const int n = n0 + c;
         // the scales come in while the MMAs run
-        const float sw = splits == 1 && n < N ? w_scale[n] : 0.0f;
+        const float sw = n < N ? w_scale[n] : 0.0f;
         for (int j = lane; j < MC; j += 32)
-            sx_s[warp - 2][j] = splits == 1 && j < tokens ? x_scale[m0 + j] : 0.0f;
+            sx_s[warp - 2][j] = j < tokens ? x_scale[m0 + j] : 0.0f;
+        if (splits > 1) sw_s[c] = sw;
         __syncwarp();
         if (!tc::mbar_wait_warp(tc::smem_u32(&acc_full), 0)) {
             give_up(status, tc::kTimeoutEpilogue, &failed);
@@ -363,19 +365,13 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
         const int tokens = min(MC, M - m0);
         const uint32_t peer0 = tc::map_shared_rank(base, 0);
         const bool wide = (N & 3) == 0;
-        // wide: channels 4 lane .. 4 lane + 3 of the tile
-        float sw[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + 4 * lane + j;
-            sw[j] = n < N ? w_scale[n] : 0.0f;
-        }
-        const int n = n0 + 4 * lane;
+        const int n = n0 + 4 * lane;          // channels 4 lane .. 4 lane + 3 of the tile
+        const float4 sw = *reinterpret_cast<const float4*>(&sw_s[4 * lane]);
         // (short code: each of these CTAs runs it a few times only, and what
         // it costs first is its instructions' way from memory)
 #pragma unroll 1
         for (int m = rank + splits * warp; m < tokens; m += splits * (kThreads / 32)) {
-            const float sx = x_scale[m0 + m];
+            const float sx = sx_s[0][m];
             const uint32_t off = static_cast<uint32_t>((m * kRows + 4 * lane) * 4);
             int4 t = tc::ld_cluster_i4(peer0 + off);
             int4 v[kMaxSplits - 1];
@@ -387,8 +383,8 @@ linear_i8_split_kernel(const __grid_constant__ CUtensorMap tmap_x,
             for (int p = 0; p < kMaxSplits - 1; ++p) {
                 t.x += v[p].x; t.y += v[p].y; t.z += v[p].z; t.w += v[p].w;
             }
-            const float o[4] = {scaled(t.x, sx, sw[0]), scaled(t.y, sx, sw[1]),
-                                scaled(t.z, sx, sw[2]), scaled(t.w, sx, sw[3])};
+            const float o[4] = {scaled(t.x, sx, sw.x), scaled(t.y, sx, sw.y),
+                                scaled(t.z, sx, sw.z), scaled(t.w, sx, sw.w)};
             YT* dst = y + static_cast<int64_t>(m0 + m) * N + n;
             if (wide) {
                 if (n < N) store4(dst, o);
@@ -442,7 +438,7 @@ template <int TN, typename YT>
 __global__ void __launch_bounds__(kPairThreads, 1)
 linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
                       const __grid_constant__ CUtensorMap tmap_w,
-                      const float* __restrict__ x_scale, const float* __restrict__ w_scale,
+                      const float* x_scale, const float* w_scale,
                       YT* __restrict__ y, int align, int M, int N, int K,
                       uint32_t* __restrict__ status) {
     using L = PairSmem<TN>;
@@ -671,16 +667,15 @@ constexpr int kVecThreads = 128;
 
 __device__ __forceinline__ int4 ld_stream_i4(const int8_t* p) {
     int4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 
 template <int MT, int R, int W, typename YT>
 __global__ void __launch_bounds__(kVecThreads)
-linear_i8_vec_kernel(const int8_t* __restrict__ x, const float* __restrict__ x_scale,
-                     const int8_t* __restrict__ w, const float* __restrict__ w_scale,
-                     YT* __restrict__ y, int M, int N, int K, int n_blocks) {
+linear_i8_vec_kernel(const int8_t* x, const float* x_scale, const int8_t* w,
+                     const float* w_scale, YT* __restrict__ y, int M, int N, int K, int n_blocks) {
     constexpr int kWarps = kVecThreads / 32;
     constexpr int U = 2;                               // pieces of a row in flight
     constexpr int kSpan = 512 * W;                     // bytes that W warps read at once
@@ -700,6 +695,12 @@ linear_i8_vec_kernel(const int8_t* __restrict__ x, const float* __restrict__ x_s
     for (int r = 0; r < R; ++r)
         if (at * 128 < K) asm volatile("prefetch.global.L2 [%0];" ::"l"(wr[r] + at * 128));
     tc::grid_dep_wait();
+    // lane m R + r will keep the sum of token m0 + m and channel n0 + r; their
+    // scales are on their way beside the operands (behind the sums: 2.7 against
+    // 2.5 us for 256 x 64 x 2048, 4.6 against 4.2 for 8 x 2048 x 4096)
+    const int my_m = m0 + lane / R, my_n = n0 + lane % R;
+    const bool have = lane < MT * R && my_m < M && my_n < N;
+    const float sx = have ? x_scale[my_m] : 0.0f, sw = have ? w_scale[my_n] : 0.0f;
     const int8_t* xr[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) xr[m] = x + static_cast<int64_t>(min(m0 + m, M - 1)) * K;
@@ -714,7 +715,7 @@ linear_i8_vec_kernel(const int8_t* __restrict__ x, const float* __restrict__ x_s
             for (int r = 0; r < R; ++r) wv[u][r] = ld_stream_i4(wr[r] + k + kSpan * u);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-                xv[u][m] = __ldg(reinterpret_cast<const int4*>(xr[m] + k + kSpan * u));
+                xv[u][m] = *reinterpret_cast<const int4*>(xr[m] + k + kSpan * u);
         }
 #pragma unroll
         for (int u = 0; u < P; ++u) {
@@ -733,15 +734,11 @@ linear_i8_vec_kernel(const int8_t* __restrict__ x, const float* __restrict__ x_s
     int k = at * 16;
     for (; k + kSpan * (U - 1) < K; k += kSpan * U) step(k, std::integral_constant<int, U>{});
     for (; k < K; k += kSpan) step(k, std::integral_constant<int, 1>{});
-    // lane m R + r keeps the sum of token m0 + m and channel n0 + r
     int mine = 0;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int t = __reduce_add_sync(kFull, acc[m][r]);
-            if (lane == m * R + r) mine = t;
-        }
+    for (int i = 0; i < MT * R; ++i) {
+        const int t = __reduce_add_sync(kFull, acc[i / R][i % R]);
+        if (lane == i) mine = t;
     }
     if constexpr (W > 1) {
         if (lane < MT * R) part[warp][lane] = mine;
@@ -752,9 +749,7 @@ linear_i8_vec_kernel(const int8_t* __restrict__ x, const float* __restrict__ x_s
             for (int i = 1; i < W; ++i) mine += part[warp + i][lane];
         }
     }
-    const int m = m0 + lane / R, n = n0 + lane % R;
-    if (lane < MT * R && m < M && n < N)
-        store1(y + static_cast<int64_t>(m) * N + n, scaled(mine, x_scale[m], w_scale[n]));
+    if (have) store1(y + static_cast<int64_t>(my_m) * N + my_n, scaled(mine, sx, sw));
 }
 
 // ---- host ------------------------------------------------------------------------

@@ -226,11 +226,18 @@ __device__ __forceinline__ double warp_sum_f64(double x) {
 // too long for that) reads them again, from the residual it has just written
 // where there is one.
 constexpr int max_threads(int ng) { return ng == 4 || ng == 8 ? 512 : 1024; }
+// Blocks of that many threads that have to fit an SM: two where fewer registers
+// than the compiler would take are faster (bf16 norm of 300 x 8192 in 6.3
+// against 8.0 us and of 4096 x 8192 in 42.1 against 43.6; rows read twice,
+// 5000 x 36000 bf16 quantised in 115 against 161, but their norm, which spills,
+// in 92 against 42 for 100 x 131056 fp32; 8192 x 2048 bf16 quantised with four
+// groups 11.0 against 10.3).
+constexpr int min_blocks(bool norm, int ng) { return ng == 1 || ng == (norm ? 4 : 0) ? 2 : 1; }
 
 template <typename XT, typename RT, bool kNorm, int NG>
-__global__ void __launch_bounds__(max_threads(NG))
-quantize_rows_kernel(const XT* __restrict__ x, const RT* residual, const float* __restrict__ weight,
-                     float eps, RT* residual_out, int8_t* __restrict__ q,
+__global__ void __launch_bounds__(max_threads(NG), min_blocks(kNorm, NG))
+quantize_rows_kernel(const XT* x, const RT* residual, const float* weight, float eps,
+                     RT* residual_out, int8_t* __restrict__ q,
                      float* __restrict__ scale, int M, int64_t D) {
     __shared__ double s_sum[32];
     __shared__ uint32_t s_max[32];
@@ -246,7 +253,8 @@ quantize_rows_kernel(const XT* __restrict__ x, const RT* residual, const float* 
     float top = 0.0f;
     // a of a group from its inputs, with its share of the statistics; the new
     // residual is written
-    auto first = [&](int g, const Raw<XT>& xr, const Raw<RT>& rr, float (&a)[kVec]) {
+    auto first = [&](int g, const Raw<XT>& xr, const Raw<RT>& rr, const Raw<float>& wr,
+                     float (&a)[kVec]) {
         const int64_t at = static_cast<int64_t>(g) * kVec;
         xr.unpack(a);
         if constexpr (kNorm) {
@@ -258,8 +266,6 @@ quantize_rows_kernel(const XT* __restrict__ x, const RT* residual, const float* 
             }
             round_to(static_cast<RT*>(nullptr), a);
             if (residual_out) store8(residual_out + base + at, a);
-            Raw<float> wr;
-            wr.load(weight + at);
             float w[kVec];
             wr.unpack(w);
 #pragma unroll
@@ -271,32 +277,46 @@ quantize_rows_kernel(const XT* __restrict__ x, const RT* residual, const float* 
 #pragma unroll
         for (int i = 0; i < kVec; i += 2) top = max_abs(top, a[i], a[i + 1]);
     };
-    constexpr int kKeep = NG > 0 ? NG : 1;
-    Raw<XT> xr[kKeep];
-    Raw<RT> rr[kKeep];
-    float keep[kKeep][kVec];
+    // The residual may be updated in place: a group is read before it is
+    // written. And what the next call of `first` reads is on its way before this
+    // one stores, since plain loads do not pass a store that may alias them.
+    auto load_x = [&](int g, Raw<XT>& xr, Raw<RT>& rr) {
+        const int64_t at = base + static_cast<int64_t>(g) * kVec;
+        xr.load(x + at);
+        if (kNorm && residual) rr.load(residual + at);
+    };
+    auto load_w = [&](int g, Raw<float>& wr) {
+        if constexpr (kNorm) wr.load(weight + static_cast<int64_t>(g) * kVec);
+    };
+    float keep[NG > 0 ? NG : 1][kVec];
     if (live) {
+        Raw<float> wr;
         if constexpr (NG > 0) {
-            // every load of the thread before its first store: the residual
-            // may be updated in place, so the compiler keeps that order
+            Raw<XT> xr[NG];
+            Raw<RT> rr[NG];
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 const int g = threadIdx.x + i * T;
-                if (g < n_groups) {
-                    xr[i].load(x + base + static_cast<int64_t>(g) * kVec);
-                    if (kNorm && residual) rr[i].load(residual + base + static_cast<int64_t>(g) * kVec);
-                }
+                if (g < n_groups) load_x(g, xr[i], rr[i]);
             }
+            Raw<float> wn;
+            if (static_cast<int>(threadIdx.x) < n_groups) load_w(threadIdx.x, wr);
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 const int g = threadIdx.x + i * T;
-                if (g < n_groups) first(g, xr[i], rr[i], keep[i]);
+                if (i + 1 < NG && g + T < n_groups) load_w(g + T, wn);
+                if (g < n_groups) first(g, xr[i], rr[i], wr, keep[i]);
+                wr = wn;
             }
         } else {
+            // (the next group's loads ahead of this one's arithmetic: 104 us
+            // against 87 for 500 x 65536 fp32)
+            Raw<XT> xr;
+            Raw<RT> rr;
             for (int g = threadIdx.x; g < n_groups; g += T) {
-                xr[0].load(x + base + static_cast<int64_t>(g) * kVec);
-                if (kNorm && residual) rr[0].load(residual + base + static_cast<int64_t>(g) * kVec);
-                first(g, xr[0], rr[0], keep[0]);
+                load_x(g, xr, rr);
+                load_w(g, wr);
+                first(g, xr, rr, wr, keep[0]);
             }
         }
     }
@@ -365,28 +385,28 @@ quantize_rows_kernel(const XT* __restrict__ x, const RT* residual, const float* 
         }
     } else {
         for (int g = threadIdx.x; g < n_groups; g += T) {
-            const int64_t at = static_cast<int64_t>(g) * kVec;
+            Raw<XT> xr;
+            Raw<RT> rr;
+            Raw<float> wr;
+            // h as this thread wrote it above, or from its parts
+            if (kNorm && residual_out) rr.load(residual_out + base + static_cast<int64_t>(g) * kVec);
+            else load_x(g, xr, rr);
+            load_w(g, wr);
             float a[kVec];
             if (kNorm && residual_out) {
-                Raw<RT> h;
-                h.load(residual_out + base + at);         // this thread wrote it above
-                h.unpack(a);
+                rr.unpack(a);
             } else {
-                xr[0].load(x + base + at);
-                xr[0].unpack(a);
+                xr.unpack(a);
                 if (kNorm && residual) {
                     float f[kVec];
-                    rr[0].load(residual + base + at);
-                    rr[0].unpack(f);
+                    rr.unpack(f);
 #pragma unroll
                     for (int i = 0; i < kVec; ++i) a[i] = __fadd_rn(a[i], f[i]);
                 }
                 if constexpr (kNorm) round_to(static_cast<RT*>(nullptr), a);
             }
             if constexpr (kNorm) {
-                Raw<float> wr;
                 float w[kVec];
-                wr.load(weight + at);
                 wr.unpack(w);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) a[i] = __fmul_rn(a[i], w[i]);
@@ -477,9 +497,8 @@ cudaError_t launch_typed(const RowsI8Args& a, cudaStream_t stream) {
 // maximum and once for its integers.
 template <bool kKeep>
 __global__ void __launch_bounds__(1024)
-gated_norm_i8_kernel(const float* __restrict__ o, const float* __restrict__ z,
-                     const float* __restrict__ norm_w, float eps, int8_t* __restrict__ q,
-                     float* __restrict__ scale, int n_groups) {
+gated_norm_i8_kernel(const float* o, const float* z, const float* norm_w, float eps,
+                     int8_t* __restrict__ q, float* __restrict__ scale, int n_groups) {
     __shared__ uint32_t s_max[32];
     tc::grid_dep_launch();
     tc::grid_dep_wait();

@@ -62,8 +62,8 @@ constexpr int kConvTile = 32;            // positions per thread in gate_conv
 // last position to scratch_ring; no separate ring pass is needed.
 template <int K, bool kWriteRing>
 __global__ void __launch_bounds__(256)
-short_conv_gate_kernel(const float* __restrict__ proj, float* ring, float* scratch_ring,
-                       const float* __restrict__ conv_w, __nv_bfloat16* __restrict__ y,
+short_conv_gate_kernel(const float* proj, float* ring, float* scratch_ring,
+                       const float* conv_w, __nv_bfloat16* __restrict__ y,
                        int64_t B, int64_t T, int64_t D, int64_t n_commit) {
     tc::grid_dep_launch();
     tc::grid_dep_wait();           // proj comes from the previous kernel
@@ -148,7 +148,7 @@ short_conv_gate_kernel(const float* __restrict__ proj, float* ring, float* scrat
 // thread's own column, so the update is safe in place.
 template <int K>
 __global__ void __launch_bounds__(256)
-short_conv_ring_kernel(const float* __restrict__ proj, float* ring, float* scratch_ring,
+short_conv_ring_kernel(const float* proj, float* ring, float* scratch_ring,
                        int64_t B, int64_t T, int64_t D, int64_t n_commit) {
     tc::grid_dep_launch();
     tc::grid_dep_wait();

@@ -69,22 +69,20 @@ __device__ __forceinline__ void load_rows(float4 (&m)[R], const float* state, Ro
 // kChannelDecay: gate holds a log-decay per key channel ([head][dk]) instead
 // of one per head.
 template <int R, bool kChannelDecay>
-__device__ __forceinline__ void update_rows(float4 (&m)[R], float* __restrict__ state,
-                                            const float* __restrict__ q,
-                                            const float* __restrict__ k,
-                                            const float* __restrict__ v,
-                                            const float* __restrict__ beta,
-                                            const float* __restrict__ gate,
-                                            float* __restrict__ out, RowTask<R> t, int Hk,
-                                            int Hv, int lane) {
+__device__ __forceinline__ void update_rows(float4 (&m)[R], float* state, const float* q,
+                                            const float* k, const float* v, const float* beta,
+                                            const float* gate, float* __restrict__ out,
+                                            RowTask<R> t, int Hk, int Hv, int lane) {
     const int64_t lb = t.head / Hv;
     const int h = static_cast<int>(t.head - lb * Hv);
     const int64_t key = (lb * Hk + (h % Hk)) * kDk + lane * 4;
-    const float4 k4 = ld_ro4(k + key);
-    const float4 q4 = ld_ro4(q + key);
+    // (plain loads: the previous kernel may have been writing these rows when
+    // this one started)
+    const float4 k4 = ld4(k + key);
+    const float4 q4 = ld4(q + key);
     float4 decay;
     if constexpr (kChannelDecay) {
-        const float4 g4 = ld_ro4(gate + t.head * kDk + lane * 4);
+        const float4 g4 = ld4(gate + t.head * kDk + lane * 4);
         decay = make_float4(expf(g4.x), expf(g4.y), expf(g4.z), expf(g4.w));
     } else {
         const float e = expf(gate[t.head]);
@@ -122,10 +120,8 @@ __device__ __forceinline__ void update_rows(float4 (&m)[R], float* __restrict__ 
 
 template <int R, bool kChannelDecay>
 __global__ void __launch_bounds__(GDN_STEP_THREADS)
-step_kernel(float* __restrict__ state, const float* __restrict__ q, const float* __restrict__ k,
-            const float* __restrict__ v, const float* __restrict__ beta,
-            const float* __restrict__ gate, float* __restrict__ out, int64_t n_tasks, int Hk,
-            int Hv) {
+step_kernel(float* state, const float* q, const float* k, const float* v, const float* beta,
+            const float* gate, float* __restrict__ out, int64_t n_tasks, int Hk, int Hv) {
     const int lane = threadIdx.x & 31;
     const int64_t warps_per_cta = blockDim.x >> 5;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * warps_per_cta;

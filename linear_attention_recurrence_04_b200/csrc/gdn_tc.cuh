@@ -240,7 +240,11 @@ __device__ __forceinline__ void tmem_ld_wait() {
 // A kernel launched with programmatic stream serialization may start while
 // the previous kernel on the stream still runs; grid_dep_wait blocks the
 // calling thread until that kernel has completed and its memory is visible.
-// Every read or write of memory an earlier kernel touches comes after it.
+// Every read or write of memory an earlier kernel touches comes after it. Such
+// memory is read through pointers without __restrict__ and never through the
+// non-coherent path (__ldg, ld.global.nc): both say that nothing writes it
+// while the kernel lives, which the previous kernel still may, and the
+// compiler may then move the load in front of the wait.
 __device__ __forceinline__ void grid_dep_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }

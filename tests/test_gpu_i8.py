@@ -301,6 +301,40 @@ def test_linear_rows_independent_of_batch():
 
 # -- as they are used ---------------------------------------------------------------
 
+@pytest.mark.parametrize("M,N,K", [(1, 512, 4096), (8, 300, 1040), (70, 200, 4096), (600, 1024, 256)])
+def test_operands_written_by_the_kernel_before(M, N, K):
+    """Each call reads what the call just before it wrote, into the same buffers
+    again and again: rows and weights in 8 bits, scales, norm weights, and a
+    product that is the next residual."""
+    g = torch.Generator().manual_seed(M + N)
+    xs = [torch.randn(M, K, generator=g).cuda() for _ in range(6)]
+    ws = [torch.randn(N, K, generator=g).cuda() for _ in range(6)]
+    q, s = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    wq, sw = torch.empty(N, K, dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda")
+    y = torch.empty(M, N, device="cuda")
+    nx = [torch.randn(M, N - N % 16, generator=g).cuda() for _ in range(6)]
+
+    def run(wait):
+        got = []
+        for x, w, r in zip(xs, ws, nx):
+            for call in (lambda: gdn.quantize_i8(x, q, s), lambda: gdn.quantize_i8(w, wq, sw),
+                         lambda: got.append(gdn.linear_i8(q, s, wq, sw, y).clone()),
+                         lambda: gdn.quantize_i8(w, wq, sw), lambda: gdn.quantize_i8(x, q, s),
+                         lambda: got.append(gdn.linear_i8(q, s, wq, sw)),
+                         # a norm whose weight the product before it wrote
+                         lambda: got.extend(gdn.add_rms_norm_i8(
+                             r, gdn.linear_i8(q[:1], s[:1], wq, sw)[0, :r.shape[1]], r))):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return got
+
+    want = run(True)
+    for _ in range(5):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
+
 def test_chain_on_a_stream_captured_and_replayed():
     """norm -> product -> quantise -> product on a side stream, captured once
     and replayed on new inputs, two graphs of other buffers interleaved."""
