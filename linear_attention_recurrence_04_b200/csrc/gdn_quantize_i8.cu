@@ -225,10 +225,15 @@ __device__ __forceinline__ double warp_sum_f64(double x) {
 // NG groups of 8 in registers between the two halves of the pass; NG = 0 (rows
 // too long for that) reads them again, from the residual it has just written
 // where there is one.
+//
+// NG depends on the number of rows, and a row's scale must not: the squares are
+// summed in an order of the row's own, by 8, then over blocks of 32 groups, then
+// over the blocks. So a warp holds NG whole blocks and sums each by itself (rows
+// read twice are summed by thread, for every number of rows).
 constexpr int max_threads(int ng) { return ng == 4 || ng == 8 ? 512 : 1024; }
 // Blocks of that many threads that have to fit an SM: two where fewer registers
 // than the compiler would take are faster (bf16 norm of 300 x 8192 in 6.3
-// against 8.0 us and of 4096 x 8192 in 42.1 against 43.6; rows read twice,
+// against 8.0 us and of 4096 x 8192 in 41.4 against 43.3; rows read twice,
 // 5000 x 36000 bf16 quantised in 115 against 161, but their norm, which spills,
 // in 92 against 42 for 100 x 131056 fp32; 8192 x 2048 bf16 quantised with four
 // groups 11.0 against 10.3).
@@ -239,7 +244,8 @@ __global__ void __launch_bounds__(max_threads(NG), min_blocks(kNorm, NG))
 quantize_rows_kernel(const XT* x, const RT* residual, const float* weight, float eps,
                      RT* residual_out, int8_t* __restrict__ q,
                      float* __restrict__ scale, int M, int64_t D) {
-    __shared__ double s_sum[32];
+    constexpr int kSums = kNorm && NG > 1 ? NG : 1;  // blocks of 32 groups a warp
+    __shared__ double s_sum[max_threads(NG) / 32 * kSums];
     __shared__ uint32_t s_max[32];
     tc::grid_dep_launch();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -247,14 +253,16 @@ quantize_rows_kernel(const XT* x, const RT* residual, const float* weight, float
     const int64_t base = row * D;
     const int T = blockDim.x;
     const int n_groups = static_cast<int>(D / kVec);
+    const int warp = threadIdx.x >> 5;              // of the row
+    const int g0 = warp * (32 * NG) + (threadIdx.x & 31);   // the thread's groups: every 32nd
     tc::grid_dep_wait();
 
-    double sum = 0.0;
+    double sums[kSums] = {};
     float top = 0.0f;
     // a of a group from its inputs, with its share of the statistics; the new
     // residual is written
     auto first = [&](int g, const Raw<XT>& xr, const Raw<RT>& rr, const Raw<float>& wr,
-                     float (&a)[kVec]) {
+                     double& sum, float (&a)[kVec]) {
         const int64_t at = static_cast<int64_t>(g) * kVec;
         xr.unpack(a);
         if constexpr (kNorm) {
@@ -278,8 +286,8 @@ quantize_rows_kernel(const XT* x, const RT* residual, const float* weight, float
         for (int i = 0; i < kVec; i += 2) top = max_abs(top, a[i], a[i + 1]);
     };
     // The residual may be updated in place: a group is read before it is
-    // written. And what the next call of `first` reads is on its way before this
-    // one stores, since plain loads do not pass a store that may alias them.
+    // written. And plain loads do not pass a store that may alias them, so that
+    // loads stand before the stores that they need not wait for.
     auto load_x = [&](int g, Raw<XT>& xr, Raw<RT>& rr) {
         const int64_t at = base + static_cast<int64_t>(g) * kVec;
         xr.load(x + at);
@@ -296,17 +304,23 @@ quantize_rows_kernel(const XT* x, const RT* residual, const float* weight, float
             Raw<RT> rr[NG];
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                const int g = threadIdx.x + i * T;
+                const int g = g0 + 32 * i;
                 if (g < n_groups) load_x(g, xr[i], rr[i]);
             }
+            // the next group's weights before this one's store where there are
+            // registers for both (4096 x 8192 fp32 in 66 us; with four groups
+            // the loads before their own store: 16384 x 2048 bf16 in 40.1
+            // against 41.4)
+            constexpr bool kAhead = NG <= 2;
             Raw<float> wn;
-            if (static_cast<int>(threadIdx.x) < n_groups) load_w(threadIdx.x, wr);
+            if (g0 < n_groups) load_w(g0, wr);
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                const int g = threadIdx.x + i * T;
-                if (i + 1 < NG && g + T < n_groups) load_w(g + T, wn);
-                if (g < n_groups) first(g, xr[i], rr[i], wr, keep[i]);
-                wr = wn;
+                const int g = g0 + 32 * i;
+                if (kAhead && i + 1 < NG && g + 32 < n_groups) load_w(g + 32, wn);
+                if (!kAhead && i > 0 && g < n_groups) load_w(g, wr);
+                if (g < n_groups) first(g, xr[i], rr[i], wr, sums[kSums > 1 ? i : 0], keep[i]);
+                if (kAhead) wr = wn;
             }
         } else {
             // (the next group's loads ahead of this one's arithmetic: 104 us
@@ -316,7 +330,7 @@ quantize_rows_kernel(const XT* x, const RT* residual, const float* weight, float
             for (int g = threadIdx.x; g < n_groups; g += T) {
                 load_x(g, xr, rr);
                 load_w(g, wr);
-                first(g, xr, rr, wr, keep[0]);
+                first(g, xr, rr, wr, sums[0], keep[0]);
             }
         }
     }
@@ -324,6 +338,8 @@ quantize_rows_kernel(const XT* x, const RT* residual, const float* weight, float
     // the row's maximum for every thread, its sum for its first warp; compared
     // as bits, where infinities and NaN are above everything
     uint32_t mbits = __float_as_uint(top);
+    double sum = sums[0];
+    const int lane = threadIdx.x & 31;
     if (T < 32) {                                   // several rows a warp, T a power of two
         for (int off = T >> 1; off > 0; off >>= 1) {
             mbits = max(mbits, __shfl_xor_sync(kFull, mbits, off));
@@ -331,20 +347,24 @@ quantize_rows_kernel(const XT* x, const RT* residual, const float* weight, float
         }
     } else {
         mbits = __reduce_max_sync(kFull, mbits);
-        if constexpr (kNorm) sum = warp_sum_f64(sum);
+        if constexpr (kNorm) sum = warp_sum_many<kSums>(sums, lane);
     }
     const int warps = T >> 5;                       // warps of a row
-    if (warps > 1) {
+    if (warps > 1 || kSums > 1) {
         const int w0 = threadIdx.y * warps;
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) {
-            s_max[w0 + (threadIdx.x >> 5)] = mbits;
-            if constexpr (kNorm) s_sum[w0 + (threadIdx.x >> 5)] = sum;
+        if (lane == 0) s_max[w0 + warp] = mbits;
+        if constexpr (kNorm) {
+            if (lane % (32 / kSums) == 0)
+                s_sum[(w0 + warp) * kSums + lane / (32 / kSums)] = sum;
         }
         __syncthreads();
         mbits = __reduce_max_sync(kFull, lane < warps ? s_max[w0 + lane] : 0u);
         if constexpr (kNorm) {
-            if (threadIdx.x < 32) sum = warp_sum_f64(lane < warps ? s_sum[w0 + lane] : 0.0);
+            if (warp == 0) {
+                sum = 0.0;
+                for (int b = lane; b < warps * kSums; b += 32) sum += s_sum[w0 * kSums + b];
+                sum = warp_sum_f64(sum);
+            }
         }
     }
     if (!live) return;
@@ -367,7 +387,7 @@ quantize_rows_kernel(const XT* x, const RT* residual, const float* weight, float
         if (plain) {
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                const int g = threadIdx.x + i * T;
+                const int g = g0 + 32 * i;
                 if (g < n_groups)
                     *reinterpret_cast<uint2*>(group(g)) =
                         kShort ? quantize8_bf16(keep[i], m, r) : quantize8(keep[i], r, far);
@@ -376,7 +396,7 @@ quantize_rows_kernel(const XT* x, const RT* residual, const float* weight, float
         if (!plain || far > kNear) {
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                const int g = threadIdx.x + i * T;
+                const int g = g0 + 32 * i;
                 if (g < n_groups) {
                     if (plain) exact(g, keep[i]);
                     else rare(g, keep[i]);

@@ -200,6 +200,76 @@ def test_rows_independent_of_batch():
         assert torch.equal(q1[0], qn[r]) and torch.equal(s1[0], sn[r])
 
 
+# Rows whose scale lies next to the middle of two fp32 numbers: adding the
+# squares in another order (by the thread of a kernel with one group of 8 a
+# thread, or with two) moves it to the other one. (seed, weight of element 0)
+AT_A_BORDER = [(1308, "0x1.4994cep+3"), (14429, "0x1.8e006cp+3"), (4424, "0x1.7f6314p+3"),
+               (10448, "0x1.787908p+3")]
+
+
+@pytest.mark.parametrize("seed,top", AT_A_BORDER)
+def test_norm_scale_independent_of_batch(seed, top):
+    """The scale of a row is the same number in every batch, to the last bit:
+    alone, below and above 2^20 groups of 8, and in each place of the batch."""
+    D = 8192
+    row = torch.randn(D, generator=torch.Generator().manual_seed(seed)).clamp(-4, 4)
+    row[0] = 1.0
+    w = torch.ones(D)
+    w[0] = float.fromhex(top)
+    row, w = row.cuda(), w.cuda()
+    q1, s1, _ = gdn.add_rms_norm_i8(row[None], w)
+    check_rows(q1, s1, *ref.rows(row.cpu().numpy()[None], None, w.cpu().numpy())[:2])
+    for M in (2, 1023, 1024, 1500):
+        q, s, _ = gdn.add_rms_norm_i8(row.expand(M, D).contiguous(), w)
+        assert torch.equal(s, s1.expand(M)) and torch.equal(q, q1.expand(M, D))
+
+
+# (types, D, the number of rows from which a thread takes more groups): the first
+# row count on the other side of 2^20 groups of 8, or of the next limit of D
+FEW_AND_MANY = [(F32, None, 8192, 1024), (F32, F32, 4112, 2041), (F32, BF16, 6000, 1399),
+                (BF16, F32, 4112, 2041), (BF16, BF16, 2048, 4096), (BF16, BF16, 2064, 4065),
+                (BF16, BF16, 8192, 1024), (BF16, BF16, 16368, 513), (F32, BF16, 16384, 512),
+                (F32, None, 1024, 8192), (BF16, BF16, 2032, 4129)]
+
+
+@pytest.mark.parametrize("xt,rt,D,M", FEW_AND_MANY)
+def test_norm_of_few_and_many_rows(xt, rt, D, M):
+    """Whole rows against the definition just below and just above the number
+    of rows from which a thread takes more of a row; the residual in place and
+    beside it; and every row the same on both sides."""
+    x = draw_rows(M, D, D + M, xt)
+    r = None if rt is None else 3 * draw_rows(M, D, D + M + 1, rt)
+    w = 1 + 0.2 * draw_rows(1, D, seed=5)[0]
+    pick = np.r_[0:4, M // 2, M - 3:M]
+    want = ref.rows(x.float().numpy()[pick], None if r is None else r.float().numpy()[pick], w.numpy(),
+                    residual_bf16=rt is BF16)
+    xc, rc, wc = x.cuda(), None if r is None else r.cuda(), w.cuda()
+    q, s, h = gdn.add_rms_norm_i8(xc, wc, rc)
+    check_rows(q[pick], s[pick], *want[:2])
+    assert rt is None or np.array_equal(h[pick].float().cpu().numpy(), want[2])
+    few = M - 1
+    r2 = None if rt is None else rc[:few].clone()
+    q2, s2, h2 = gdn.add_rms_norm_i8(xc[:few], wc, r2, r2)
+    assert torch.equal(q2, q[:few]) and torch.equal(s2, s[:few])
+    assert rt is None or (h2 is r2 and torch.equal(h2, h[:few]))
+    if rt is not None:                                   # the large batch in place too
+        q2, s2, _ = gdn.add_rms_norm_i8(xc, wc, rc, rc)
+        assert torch.equal(q2, q) and torch.equal(s2, s) and torch.equal(rc, h)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,M", [(512, 16384), (528, 15888), (1008, 8323), (1024, 8192), (4096, 2048),
+                                 (8208, 1023), (16368, 513)])
+def test_quantize_few_and_many_rows(D, M, dtype):
+    x = draw_rows(M, D, D + M, dtype)
+    pick = np.r_[0:4, M // 2, M - 3:M]
+    xc = x.cuda()
+    q, s = gdn.quantize_i8(xc)
+    check_rows(q[pick], s[pick], *ref.rows(x.float().numpy()[pick])[:2])
+    q2, s2 = gdn.quantize_i8(xc[:M - 1])
+    assert torch.equal(q2, q[:M - 1]) and torch.equal(s2, s[:M - 1])
+
+
 # -- the product ------------------------------------------------------------------
 
 def draw_product(M, N, K, seed):
