@@ -480,13 +480,18 @@ cudaError_t launch_rows(const RowsI8Args& a, cudaStream_t stream) {
 }
 
 // Groups a thread. Few rows: one, so that a row is spread over as many threads
-// as there are (64 x 2048 in 2.3 us against 4.3 with four). Many rows (a
-// million threads with one group each, some three waves): as many as put 64 to
-// 128 bytes a thread on their way, since what a row costs beside its elements
-// is shared by fewer threads (4096 x 8192 bf16 quantised: 22.7 with four,
-// 31.7 with one; bf16 norm 40.9 against 50.8; but fp32 norm of 4096 x 4096
-// 39.4 with four, 35.9 with one, and of 4096 x 8192 75.4 with two, 88.7 with
-// one).
+// as there are (norm of 64 x 2048 in 2.2 us against 2.5 with two and 4.5 with
+// four, of 1000 x 2048 bf16 4.7 against 5.0 and 7.2). Many rows (a million
+// threads with one group each, some three waves): as many as put 64 to 128 bytes
+// a thread on their way, since what a row costs beside its elements is shared by
+// fewer threads (4096 x 8192 bf16 quantised: 20.4 with four, 30.3 with one; bf16
+// norm 41.1 against 49.9; fp32 norm 65.6 with two, 67.3 with one and 88 with
+// four, which is left out).
+// Where the limit is not the best choice: bf16 norm of 4096 x 2048 takes 15.0
+// with four and 13.1 with one; quantising rows of middle length below a million
+// groups is faster with two (1000 x 6000 bf16 7.3 against 5.5, fp32 8.7 against
+// 7.4; 1024 x 4096 fp32 5.5 against 5.4), and 16384 x 512 fp32 with four (8.2
+// against 6.0).
 template <typename XT, typename RT, bool kNorm>
 int groups_a_thread(int64_t M, int64_t groups) {
     const int least = groups <= 1024 ? 1 : groups <= 2048 ? 2 : groups <= 4096 ? 8 : 0;
@@ -504,7 +509,10 @@ cudaError_t launch_typed(const RowsI8Args& a, cudaStream_t stream) {
     switch (ng) {
         case 1: return launch_rows<XT, RT, kNorm, 1>(a, stream);
         case 2: return launch_rows<XT, RT, kNorm, 2>(a, stream);
-        case 4: return launch_rows<XT, RT, kNorm, 4>(a, stream);
+        case 4:
+            if constexpr (!kNorm || sizeof(XT) + sizeof(RT) == 4)
+                return launch_rows<XT, RT, kNorm, 4>(a, stream);
+            return cudaErrorInvalidValue;             // (never chosen for fp32 norms)
         case 8: return launch_rows<XT, RT, kNorm, 8>(a, stream);
         default: return launch_rows<XT, RT, kNorm, 0>(a, stream);
     }
