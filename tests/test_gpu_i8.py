@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import i8_reference as ref
+import i8_shapes
 import oracle
 from linear_attention_recurrence_04_b200 import gdn, inputs
 from parity import assert_parity
@@ -305,6 +306,24 @@ def check_product(M, N, K, dtype, seed=0, rows=None):
 ])
 def test_linear(M, N, K, dtype):
     check_product(M, N, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K,tile,splits", i8_shapes.SPLIT)
+def test_linear_split(M, N, K, tile, splits, dtype):
+    check_product(M, N, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K,tokens,warps", i8_shapes.VEC)
+def test_linear_vec(M, N, K, tokens, warps, dtype):
+    check_product(M, N, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K,tile", i8_shapes.PAIR)
+def test_linear_pair(M, N, K, tile, dtype):
+    check_product(M, N, K, dtype, rows=sorted({*range(0, M, 29), *range(250, 262), M - 2, M - 1}))
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
