@@ -1,6 +1,8 @@
 """The choice of gdn_linear_i8's kernels (csrc/gdn_linear_i8_plan.h, plain host
 code) over the sizes it accepts, and that the shapes of the tests reach every
 kernel that it can choose."""
+import ast
+import os
 import random
 import subprocess
 
@@ -98,3 +100,15 @@ def test_other_numbers_of_sms(plan):
         for (M, N, K), (form, tile, splits, _) in zip(shapes, plan(shapes, sms)):
             assert form in (VEC, SPLIT, PAIR)
             assert form != SPLIT or (tile in (16, 32, 64, 128) and splits in (1, 2, 4, 8))
+
+
+def test_smoke_reaches_every_form(plan):
+    """The shapes that __graft_entry__.smoke() runs."""
+    with open(os.path.join(gdn_build.ROOT, "__graft_entry__.py")) as f:
+        tree = ast.parse(f.read())
+    lists = [n.value for n in ast.walk(tree) if isinstance(n, ast.Assign)
+             and any(getattr(t, "id", "") == "I8_SHAPES" for t in n.targets)]
+    shapes = ast.literal_eval(lists[0])
+    got = plan(shapes)
+    assert {p[0] for p in got} == {VEC, SPLIT, PAIR}
+    assert {p[2] > 1 for p in got if p[0] == SPLIT} == {True}
