@@ -712,3 +712,19 @@ def test_offsets_past_32_bits():
     q, s = gdn.quantize_i8(xb)
     check_rows(q[-5:], s[-5:], *ref.rows(x.float().numpy())[:2])
     assert int(torch.count_nonzero(q[:-5])) == 0 and int(torch.count_nonzero(s[:-5])) == 0
+
+
+@pytest.mark.parametrize("M,K", [(3, 2048), (40, 528), (300, 4112)])
+def test_one_tensor_for_two_arguments(M, K):
+    """Rows against themselves, and a row added to itself."""
+    x = draw_rows(M, K, 77)
+    xc = x.cuda()
+    q, s = gdn.quantize_i8(xc)
+    y = gdn.linear_i8(q, s, q, s)
+    qn, sn = q.cpu().numpy(), s.cpu().numpy()
+    assert np.array_equal(y.cpu().numpy(), ref.linear(qn, sn, qn, sn))
+    w = torch.ones(K)
+    got = gdn.add_rms_norm_i8(xc, w.cuda(), xc)
+    want = ref.rows(x.numpy(), x.numpy(), w.numpy())
+    check_rows(got[0], got[1], *want[:2])
+    assert np.array_equal(got[2].cpu().numpy(), want[2]) and torch.equal(xc.cpu(), x)
