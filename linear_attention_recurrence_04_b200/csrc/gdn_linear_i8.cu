@@ -11,7 +11,7 @@
 //
 //   vec    up to four tokens, and small products: dp4a on plain loads, no
 //          barrier; bound by the weights' way from HBM (1 x 8192 x 8192 in
-//          12.7 us, 5.3 TB/s) or by latency (1 x 64 x 2048 in 1.3 us);
+//          11.9 us, 5.7 TB/s) or by latency (1 x 64 x 2048 in 1.0 us);
 //   split  tiles of 128 channels x 16 .. 128 tokens, one a CTA, K divided over
 //          the CTAs of a cluster where there are few tiles: the weights are
 //          the MMA's A operand, so that its width follows the tokens, and a
@@ -23,10 +23,10 @@
 //          persistent, a tile stored while the next one is formed: the tokens
 //          are the A operand, so that a lane holds a token's neighbouring
 //          channels and stores whole sectors. Bound by the tensor pipe at the
-//          clock that the power limit leaves (8192^3 bf16 out: 508 k cycles
-//          against 459 k of MMA work, 1.55 GHz, 340 us = 3.2 POP/s), with
-//          short K by the stores beside it (16384 x 8192 x 2048: 181 us bf16,
-//          216 us fp32 out).
+//          clock that the power limit leaves (8192^3 bf16 out, one cold call:
+//          517 k cycles, 459 k of them MMA work, in 332 us, so 1.56 GHz and
+//          3.3 POP/s), with short K by the stores beside it (16384 x 8192 x
+//          2048: 174 to 181 us bf16, 213 to 256 us fp32 out, by that clock).
 //
 // What the loops cost decides the short kernels. An MMA of K = 32 bytes takes
 // N / 2 cycles (at least 45), but a loop of one thread chosen by its lane
@@ -136,7 +136,7 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
 // at token 0's first one, `channels` and `left` tokens of them exist. `even`
 // (N and y allow two channels at once): neighbouring lanes trade, so that a
 // store covers two tokens with half as many stores (6000 x 1998 x 64 bf16 in
-// 17.2 us against 21.4).
+// 17.3 us against 21.4).
 template <int kTokens, typename YT>
 __device__ __forceinline__ void store_columns(YT* y, const float (&v)[kTokens], int64_t N,
                                               int channels, int left, int lane, bool even) {
@@ -862,8 +862,9 @@ cudaError_t launch_vec_w(const LinearI8Args& a, cudaStream_t stream) {
 }
 
 // R rows a warp: as many as keep its loads few without leaving it too few in
-// flight (8 x 2048 x 4096: 4.1 with 4 against 4.3 with 2; 8 x 4096 x 2048:
-// 4.4 with 2; 1 x 1000 x 10000: 3.7 with 2, 5.2 with 4).
+// flight (8 x 2048 x 4096: 4.2 with 4 against 4.6 with 2; 1 x 1000 x 10000: 3.4
+// with 2, 4.6 with 4). Where another number is better: 8 x 4096 x 2048 takes 4.5
+// with 2 and 4.1 with 4.
 template <typename YT>
 cudaError_t launch_vec(const LinearI8Args& a, cudaStream_t stream) {
     if (a.M <= 1) return launch_vec_w<1, 2, YT>(a, stream);

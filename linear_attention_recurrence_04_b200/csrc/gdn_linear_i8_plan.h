@@ -10,8 +10,9 @@ constexpr int kI8TileChannels = 128;   // output channels of a split tile
 constexpr int kI8MaxSplits = 8;        // CTAs of a cluster that share a split tile
 
 // W warps share a row so that long rows are on their way at once: at one
-// token 2048 x 4096 takes 2.7 with 4, 2.8 with 2 and 3.7 with one,
-// 4096 x 2048 3.0 (R = 4: 2.5), 2.6 and 3.1, 2048 x 512 1.7, 1.6 and 1.5.
+// token 2048 x 4096 takes 2.4 with 4, 2.6 with 2 and 4.2 with one,
+// 4096 x 2048 3.3, 2.4 and 3.5, 2048 x 512 1.7, 1.5 and 1.3. Where another
+// number is better: 8 tokens of 4096 x 2048 take 4.5 with 2 and 3.8 with one.
 inline int vec_warps(int64_t K) { return K >= 4096 ? 4 : K >= 1024 ? 2 : 1; }
 
 // Which kernel takes a product.
@@ -26,15 +27,15 @@ struct PlanI8 {
 // 16384 x 8192 x 2048; sums are exact, so the choice never shows in a result).
 //   vec    a wave of warps (16 an SM) takes 0.4 + 0.39 per 1000 bytes of its
 //          rows, after 1.1: 256 x 64 x 2048 in 2.5 against 3.6 (split), but
-//          64 x 1024 x 1024 in 3.6 against 3.1. Calls of at most 4 tokens
+//          64 x 1024 x 1024 in 3.6 against 3.3. Calls of at most 4 tokens
 //          always: 1 x 8192 x 2048 in 3.7 against 5.5.
 //   split  a wave of CTAs starts and ends in 1.75 .. 2.9 and spends 0.27 ..
 //          0.5 on 256 bytes of K; adding over a cluster costs 1.6 .. 2.9 more:
-//          16 x 256 x 8192 in 4.6 with 8 CTAs against 10 with one, but
+//          16 x 256 x 8192 in 4.3 with 8 CTAs against 10 with one, but
 //          64 x 4096 x 2048 in 6.0 with 4 against 5.0 with one.
 //   pair   starts and ends once, 4.9 or 5.6, and overlaps its tiles:
 //          1024 x 8192 x 2048 in 18.2 against 29.5 (split), but
-//          256 x 4096 x 2048 in 7.7 against 5.7.
+//          256 x 4096 x 2048 in 7.7 against 5.8.
 inline PlanI8 plan_i8(int64_t M, int64_t N, int64_t K, int64_t sms) {
     if (M <= 4) return {PlanI8::kVec, 0, 0};
     const auto waves = [](int64_t n, int64_t at_once) {

@@ -19,14 +19,16 @@
 // in double. The squares are summed in double: no row of finite values
 // overflows, and the scale is rounded to fp32 once.
 //
-// Bound by HBM for many rows: 16384 x 2048 fp32 with an fp32 residual 66.7 us
-// (6.5 TB/s of the 6.46 a copy reaches), 16384 x 4096 fp32 quantised 49.9 us;
-// bf16 rows, with half the bytes for the same instructions, 40.0 us for
-// 16384 x 2048 with a bf16 residual (5.9 TB/s) and 12.0 us for 8192 x 2048
-// quantised (4.2 TB/s; some 2 us of that is the launch's start and end). Few
-// rows are bound by latency: one row of 2048 takes 1.9 us. Rows fetched ahead
-// by persistent blocks (the next row's loads in registers) were slower: 12.7
-// and 55 us for the two bf16 shapes, for want of registers.
+// Bound by HBM for many rows: 16384 x 2048 fp32 with an fp32 residual in 64.6 us,
+// 16384 x 4096 fp32 quantised in 49.6. (Of the 436 and 336 MB that these move
+// 395 and 318 cross the DRAM pins before the kernel ends, 6.0 and 6.4 TB/s of the
+// 6.46 of a copy; the last of the writes are still in the L2 then.) bf16 rows,
+// with half the bytes for the same instructions, are bound by issue: 40.1 us for
+// 16384 x 2048 with a bf16 residual, 10.7 us for 8192 x 2048 quantised, some 2 us
+// of that the launch's start and end. Few rows are bound by latency: one row of
+// 2048 takes 1.9 us. Rows fetched ahead by persistent blocks (the next row's loads
+// in registers) were slower, for want of registers: by 2 % quantising and 40 %
+// with the norm for the two bf16 shapes.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -104,9 +106,9 @@ constexpr float kNear = 0.5f - 0x1p-16f;
 constexpr float kMagic = 12582912.0f;           // 1.5 * 2^23: a sum's low bits are rint
 
 // Two fp32 values in a 64-bit register and the packed operations on them: each
-// an issue slot for both. bf16 rows are bound by issue (30000 x 1024 in 18.5
-// us against 19.6); for the fp32 norm the registers that they pair cost more
-// (16384 x 2048 in 70.8 against 66.7).
+// an issue slot for both. bf16 rows are bound by issue (6 % less time for
+// 30000 x 1024); for the fp32 norm the registers that they pair cost more (6 %
+// more time for 16384 x 2048).
 struct F2 {
     uint64_t v;
     __device__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
